@@ -15,6 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libllattn.so")
 
 F32, BF16 = 0, 1
+NORMS = {"l2": 0, "rms": 1}
+LAYOUTS = {"half": 0, "interleaved": 1}
 PATHS = {"auto": 0, "simt": 1, "tcgen05": 2, "tcgen05_serial": 3}
 
 # Every symbol include/llattn.h declares.
@@ -25,7 +27,10 @@ EXPORTS = (
     "llattn_fwd_noalloc", "llattn_decode_state_bytes", "llattn_decode_step",
     "llattn_bwd_workspace_bytes", "llattn_bwd", "llattn_fwd_bf16", "llattn_stream_status",
     "llattn_segment_plan", "llattn_set_segment_chunks", "llattn_gdn_fwd",
-    "llattn_prefill_state",
+    "llattn_prefill_state", "llattn_qk_norm_rope", "llattn_qk_norm_rope_bwd_workspace_bytes",
+    "llattn_qk_norm_rope_bwd", "llattn_glr_fwd", "llattn_glr_bwd",
+    "llattn_decode_q8_state_bytes", "llattn_decode_step_q8", "llattn_prefill_state_q8",
+    "llattn_read_state_q8",
 )
 
 NOALLOC_SCRATCH_BYTES = 32 << 20  # LLATTN_NOALLOC_SCRATCH_BYTES
@@ -94,6 +99,27 @@ def lib():
     L.llattn_segment_plan.argtypes = [i, i, i, i, i, i, ctypes.POINTER(ctypes.c_int)]
     L.llattn_set_segment_chunks.restype = i
     L.llattn_set_segment_chunks.argtypes = [i]
+    ll, sz, fl, szp = ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
+    L.llattn_qk_norm_rope.restype = i
+    L.llattn_qk_norm_rope.argtypes = [i, vp, vp, ll, ll, f_p, f_p, i_p, f_p, vp, vp, ll, i, i, i, i,
+                                      i, i, i, fl, vp]
+    L.llattn_qk_norm_rope_bwd_workspace_bytes.restype = i
+    L.llattn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i, i, szp]
+    L.llattn_qk_norm_rope_bwd.restype = i
+    L.llattn_qk_norm_rope_bwd.argtypes = [i, vp, vp, ll, ll, f_p, f_p, i_p, f_p, f_p, f_p, f_p, f_p,
+                                          ll, ll, f_p, f_p, ll, i, i, i, i, i, i, i, fl, vp, sz, vp]
+    L.llattn_glr_fwd.restype = i
+    L.llattn_glr_fwd.argtypes = [i, vp, f_p, f_p, f_p, f_p, i, i, i, i_p, vp]
+    L.llattn_glr_bwd.restype = i
+    L.llattn_glr_bwd.argtypes = [f_p] * 8 + [i, i, i, i_p, vp]
+    L.llattn_decode_q8_state_bytes.restype = i
+    L.llattn_decode_q8_state_bytes.argtypes = [i, i, i, i, i, szp]
+    L.llattn_decode_step_q8.restype = i
+    L.llattn_decode_step_q8.argtypes = [i, vp, vp, vp, f_p, f_p, i_p, vp, f_p, i, i, i, i, i, vp]
+    L.llattn_prefill_state_q8.restype = i
+    L.llattn_prefill_state_q8.argtypes = [i, vp, vp, f_p, vp, i, i, i, i, i, i, i_p, vp]
+    L.llattn_read_state_q8.restype = i
+    L.llattn_read_state_q8.argtypes = [vp, i_p, vp, i, i, i, i, i, i, vp]
     L.llattn_profile.restype = i
     L.llattn_profile.argtypes = [i]
     L.llattn_profile_read.restype = i
@@ -400,3 +426,315 @@ def stream_status(clear: bool = True, stream=None) -> int:
     if st not in (0, 6):
         _check(st, "llattn_stream_status")
     return int(flags.value)
+
+
+def _on_device(fn, dev, stream, where, args):
+    """The C call `fn(*args, stream)` with `dev`, the tensors' device, current."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    _check(st, where)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _in_dtype(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise TypeError("inputs must be bf16 or fp32")
+
+
+def _expect(t, name, dtype, shape, dev, contiguous=True):
+    """Type, device, shape (None: any) and contiguity of an argument that may be absent."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _token_rows(t, name):
+    """(tokens, rows per token, d, stride of a token) of a tensor [..., rows, d] whose rows lie
+    side by side and whose tokens are one stride apart."""
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be [..., rows, d]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    G, d = shape[-2], shape[-1]
+    n = 1
+    for x in shape[:-2]:
+        n *= x
+    if n * G * d and (stride[-1] != 1 or (G > 1 and stride[-2] != d)):
+        raise ValueError(f"{name}'s rows must lie side by side")
+    step, span = None, 1   # of the dimensions with more than one entry, the inner ones seen so far
+    for x, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+        if x == 1:
+            continue
+        if step is None:
+            step = st
+        elif n and st != step * span:
+            raise ValueError(f"{name}'s tokens must be one stride apart")
+        span *= x
+    return n, G, d, step if step is not None and n > 1 else G * d
+
+
+def _qk_args(q, k, wq, wk, pos, inv_freq, heads, norm, layout):
+    import torch
+    dt = _in_dtype(q)
+    if k.dtype != q.dtype:
+        raise TypeError("q and k must share a dtype")
+    n, Gq, d, qs = _token_rows(q, "q")
+    nk, Gk, dk, ks = _token_rows(k, "k")
+    if k.shape[:-2] != q.shape[:-2] or dk != d:
+        raise ValueError("q and k must have the same tokens and row length")
+    dev = q.device
+    if k.device != dev:
+        raise ValueError(f"k must be on {dev}")
+    _expect(wq, "wq", torch.float32, (d,), dev)
+    _expect(wk, "wk", torch.float32, (d,), dev)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _expect(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev)
+        if pos is None:
+            raise ValueError("a rotation needs pos")
+        _expect(pos, "pos", torch.int32, None, dev)
+        if pos.numel() != n:
+            raise ValueError("pos must have one entry for each token")
+    if norm not in NORMS or layout not in LAYOUTS:
+        raise ValueError(f"norm is one of {tuple(NORMS)}, layout one of {tuple(LAYOUTS)}")
+    return dt, n, Gq, Gk, d, qs, ks, rot, heads if heads is not None else max(Gq, Gk)
+
+
+def qk_norm_rope(q, k, *, wq=None, wk=None, pos=None, inv_freq=None, heads: Optional[int] = None,
+                 norm: str = "l2", layout: str = "half", eps: float = 1e-6, out=None, stream=None):
+    """Norms of q and k rows with the position rotation (llattn_qk_norm_rope): returns (qo, ko).
+
+    q [..., Gq, d], k [..., Gk, d] bf16 or fp32; rows of a token side by side, tokens one stride
+    apart (slices of a projection's output do).  heads: rows each token has in the outputs
+    [..., heads, d] (default: the larger of Gq, Gk); each group is written to heads / G of them.
+    wq, wk fp32 [d]; inv_freq fp32 [rot/2] with pos int32, one entry per token, or None."""
+    import torch
+    dt, n, Gq, Gk, d, qs, ks, rot, H = _qk_args(q, k, wq, wk, pos, inv_freq, heads, norm, layout)
+    dev, shape = q.device, q.shape[:-2] + (H, d)
+    if out is None:
+        out = (torch.empty(shape, dtype=q.dtype, device=dev),
+               torch.empty(shape, dtype=q.dtype, device=dev))
+    else:
+        _expect(out[0], "out[0]", q.dtype, shape, dev)
+        _expect(out[1], "out[1]", q.dtype, shape, dev)
+    _on_device(lib().llattn_qk_norm_rope, dev, stream, "llattn_qk_norm_rope",
+               (dt, _ptr(q), _ptr(k), qs, ks, _ptr(wq), _ptr(wk), _ptr(pos) if rot else None,
+                _ptr(inv_freq), _ptr(out[0]), _ptr(out[1]), n, Gq, Gk, H, d, rot,
+                LAYOUTS[layout], NORMS[norm], eps))
+    return out
+
+
+def qk_norm_rope_backward(q, k, dqo, dko, *, wq=None, wk=None, pos=None, inv_freq=None,
+                          norm: str = "l2", layout: str = "half", eps: float = 1e-6, grads=None,
+                          workspace=None, stream=None):
+    """Gradients of qk_norm_rope from those at its outputs (llattn_qk_norm_rope_bwd).
+
+    q, k, wq, wk, pos, inv_freq, norm, layout, eps as in the forward; dqo, dko fp32
+    [..., heads, d].  Returns a dict of fp32 tensors q, k and, where weights are given, wq, wk (or
+    fills `grads`, a dict of preallocated ones; its q and k may be strided as the inputs may)."""
+    import torch
+    heads = dqo.shape[-2] if dqo.dim() >= 3 else None
+    dt, n, Gq, Gk, d, qs, ks, rot, H = _qk_args(q, k, wq, wk, pos, inv_freq, heads, norm, layout)
+    dev, f32 = q.device, torch.float32
+    _expect(dqo, "dqo", f32, q.shape[:-2] + (H, d), dev)
+    _expect(dko, "dko", f32, q.shape[:-2] + (H, d), dev)
+    if grads is None:
+        grads = {"q": torch.empty(q.shape, dtype=f32, device=dev),
+                 "k": torch.empty(k.shape, dtype=f32, device=dev)}
+        if wq is not None:
+            grads["wq"] = torch.empty(d, dtype=f32, device=dev)
+        if wk is not None:
+            grads["wk"] = torch.empty(d, dtype=f32, device=dev)
+        dqs, dks = Gq * d, Gk * d
+    else:
+        _expect(grads["q"], "grads['q']", f32, q.shape, dev, contiguous=False)
+        _expect(grads["k"], "grads['k']", f32, k.shape, dev, contiguous=False)
+        _expect(grads.get("wq"), "grads['wq']", f32, (d,), dev)
+        _expect(grads.get("wk"), "grads['wk']", f32, (d,), dev)
+        dqs, dks = _token_rows(grads["q"], "grads['q']")[3], _token_rows(grads["k"], "grads['k']")[3]
+    ws_n = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _on_device(lib().llattn_qk_norm_rope_bwd, dev, stream, "llattn_qk_norm_rope_bwd",
+               (dt, _ptr(q), _ptr(k), qs, ks, _ptr(wq), _ptr(wk), _ptr(pos) if rot else None,
+                _ptr(inv_freq), _ptr(dqo), _ptr(dko), _ptr(grads["q"]), _ptr(grads["k"]), dqs, dks,
+                _ptr(grads.get("wq")), _ptr(grads.get("wk")), n, Gq, Gk, H, d, rot,
+                LAYOUTS[layout], NORMS[norm], eps, _ptr(workspace), ws_n))
+    return grads
+
+
+def qk_norm_rope_bwd_workspace_bytes(d: int, weights: bool = True) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().llattn_qk_norm_rope_bwd_workspace_bytes(int(d), int(weights), ctypes.byref(n)),
+           "llattn_qk_norm_rope_bwd_workspace_bytes")
+    return int(n.value)
+
+
+def _glr_shape(t, cu_seqlens, T):
+    """(B, T, D) of [B, T, ...channels], or [total, ...channels] with cu_seqlens."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("inputs must be CUDA tensors")
+    if cu_seqlens is None:
+        if t.dim() < 3:
+            raise ValueError("dense inputs are [B, T, ...channels]")
+        B, T, rest = t.shape[0], t.shape[1], t.shape[2:]
+    else:
+        _expect(cu_seqlens, "cu_seqlens", torch.int32, None, t.device)
+        if T is None:
+            raise ValueError("packed inputs need T (the bound on every length)")
+        if t.dim() < 2 or cu_seqlens.numel() < 1:
+            raise ValueError("packed inputs are [total, ...channels] with cu_seqlens [B + 1]")
+        B, rest = cu_seqlens.numel() - 1, t.shape[1:]
+        T = T if t.shape[0] else 0   # no rows at all: every sequence is empty
+    return B, T, rest.numel(), (B,) + tuple(rest)
+
+
+def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[int] = None,
+                out=None, stream=None):
+    """The gated linear recurrence h_t = exp(log_a_t) h_{t-1} + x_t (llattn_glr_fwd): returns h (fp32).
+
+    x bf16 or fp32 and log_a fp32, both [B, T, ...channels], or [total, ...channels] with
+    cu_seqlens and T.  h0 [B, ...channels] fp32 is the state carried in; h_last, a preallocated
+    tensor of the same shape (h0 itself will do), receives the state after the last token."""
+    import torch
+    dt, (B, T, D, state) = _in_dtype(x), _glr_shape(x, cu_seqlens, T)
+    dev, f32 = x.device, torch.float32
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _expect(log_a, "log_a", f32, x.shape, dev)
+    for t, n in ((h0, "h0"), (h_last, "h_last")):
+        _expect(t, n, f32, None, dev)
+        if t is not None and t.numel() != B * D:
+            raise ValueError(f"{n} must have shape {state}")
+    if out is None:
+        out = torch.empty(x.shape, dtype=f32, device=dev)
+    else:
+        _expect(out, "out", f32, x.shape, dev)
+    _on_device(lib().llattn_glr_fwd, dev, stream, "llattn_glr_fwd",
+               (dt, _ptr(x), _ptr(log_a), _ptr(h0), _ptr(out), _ptr(h_last), B, T, D,
+                _ptr(cu_seqlens)))
+    return out
+
+
+def glr_backward(log_a, h, dh, *, h0=None, dh_last=None, cu_seqlens=None, T: Optional[int] = None,
+                 grads=None, stream=None):
+    """Gradients of glr_forward from dh (and dh_last) through llattn_glr_bwd.
+
+    log_a, h (the forward's output), dh fp32, shaped as in the forward; h0, dh_last fp32
+    [B, ...channels] or None.  Returns a dict of fp32 tensors x, log_a and, where h0 is given, h0
+    (or fills `grads`, a dict of preallocated ones)."""
+    import torch
+    B, T, D, state = _glr_shape(log_a, cu_seqlens, T)
+    dev, f32 = log_a.device, torch.float32
+    _expect(log_a, "log_a", f32, None, dev)
+    _expect(h, "h", f32, log_a.shape, dev)
+    _expect(dh, "dh", f32, log_a.shape, dev)
+    for t, n in ((h0, "h0"), (dh_last, "dh_last")):
+        _expect(t, n, f32, None, dev)
+        if t is not None and t.numel() != B * D:
+            raise ValueError(f"{n} must have shape {state}")
+    if grads is None:
+        grads = {"x": torch.empty(log_a.shape, dtype=f32, device=dev),
+                 "log_a": torch.empty(log_a.shape, dtype=f32, device=dev)}
+        if h0 is not None:
+            grads["h0"] = torch.empty(h0.shape, dtype=f32, device=dev)
+    else:
+        _expect(grads["x"], "grads['x']", f32, log_a.shape, dev)
+        _expect(grads["log_a"], "grads['log_a']", f32, log_a.shape, dev)
+        t = grads.get("h0")
+        _expect(t, "grads['h0']", f32, None, dev)
+        if t is not None and t.numel() != B * D:
+            raise ValueError(f"grads['h0'] must have shape {state}")
+    _on_device(lib().llattn_glr_bwd, dev, stream, "llattn_glr_bwd",
+               (_ptr(log_a), _ptr(h), _ptr(h0), _ptr(dh), _ptr(dh_last), _ptr(grads["x"]),
+                _ptr(grads["log_a"]), _ptr(grads.get("h0")), B, T, D, _ptr(cu_seqlens)))
+    return grads
+
+
+def decode_q8_state_bytes(B: int, H: int, L: int, dk: int, dv: int) -> int:
+    """Bytes of the 8-bit decoding state buffer (llattn_decode_q8_state_bytes)."""
+    n = ctypes.c_size_t(0)
+    _check(lib().llattn_decode_q8_state_bytes(int(B), int(H), int(L), int(dk), int(dv),
+                                              ctypes.byref(n)), "llattn_decode_q8_state_bytes")
+    return int(n.value)
+
+
+def _q8_state(state, B, H, L, dk, dv):
+    if not state.is_cuda or not state.is_contiguous():
+        raise ValueError("state must be a contiguous CUDA tensor")
+    need = decode_q8_state_bytes(B, H, L, dk, dv)
+    if state.numel() * state.element_size() < need:
+        raise ValueError(f"state must hold {need} bytes")
+    return state.device
+
+
+def decode_step_q8(q, k, v, log_a, lam, pos, state, out, B, H, L, dk, dv, stream=None):
+    """llattn_decode_step_q8: decode_step on the 8-bit state (a buffer of decode_q8_state_bytes()
+    bytes, of any dtype).  q, k [B,H,dk] and v [B,H,dv] bf16 or fp32, log_a [B,H] and lam [B,H,L]
+    fp32, pos int32 [B], out fp32 [B,H,dv]."""
+    import torch
+    dt, dev, f32 = _in_dtype(q), _q8_state(state, B, H, L, dk, dv), torch.float32
+    _expect(q, "q", q.dtype, (B, H, dk), dev)
+    _expect(k, "k", q.dtype, (B, H, dk), dev)
+    _expect(v, "v", q.dtype, (B, H, dv), dev)
+    _expect(log_a, "log_a", f32, (B, H), dev)
+    _expect(lam, "lam", f32, (B, H, L), dev)
+    _expect(pos, "pos", torch.int32, (B,), dev)
+    _expect(out, "out", f32, (B, H, dv), dev)
+    _on_device(lib().llattn_decode_step_q8, dev, stream, "llattn_decode_step_q8",
+               (dt, _ptr(q), _ptr(k), _ptr(v), _ptr(log_a), _ptr(lam), _ptr(pos), _ptr(state),
+                _ptr(out), B, H, L, dk, dv))
+    return out
+
+
+def prefill_state_q8(k, v, log_a, state, B, H, T, L, dk, dv, cu_seqlens=None, stream=None):
+    """llattn_prefill_state_q8: prefill_state into the 8-bit state.  k, v dense [B,T,H,d] or packed
+    [total,H,d] (bf16 or fp32), log_a fp32 [..,H], cu_seqlens int32 [B+1] or None."""
+    import torch
+    dt, dev = _in_dtype(k), _q8_state(state, B, H, L, dk, dv)
+    lead = (B, T) if cu_seqlens is None else (k.shape[0],)
+    _expect(k, "k", k.dtype, lead + (H, dk), dev)
+    _expect(v, "v", k.dtype, lead + (H, dv), dev)
+    _expect(log_a, "log_a", torch.float32, lead + (H,), dev)
+    _expect(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    _on_device(lib().llattn_prefill_state_q8, dev, stream, "llattn_prefill_state_q8",
+               (dt, _ptr(k), _ptr(v), _ptr(log_a), _ptr(state), B, H, T, L, dk, dv,
+                _ptr(cu_seqlens)))
+    return state
+
+
+def read_state_q8(state, B, H, L, dk, dv, slot=None, out=None, dtype=None, stream=None):
+    """llattn_read_state_q8: the values an 8-bit state holds, [B,H,L-1,dk,dv], or with slot (int32
+    [B]) those of one slot of each sequence, [B,H,dk,dv]; bf16 (the default) and fp32 are exact."""
+    import torch
+    dev = _q8_state(state, B, H, L, dk, dv)
+    _expect(slot, "slot", torch.int32, (B,), dev)
+    shape = (B, H, dk, dv) if slot is not None else (B, H, L - 1, dk, dv)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
+    else:
+        _expect(out, "out", out.dtype, shape, dev)
+    _on_device(lib().llattn_read_state_q8, dev, stream, "llattn_read_state_q8",
+               (_ptr(state), _ptr(slot), _ptr(out), _in_dtype(out), B, H, L, dk, dv))
+    return out

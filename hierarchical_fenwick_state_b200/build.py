@@ -17,9 +17,14 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["llattn_api.cu", "llattn_simt.cu", "llattn_tc.cu", "llattn_noalloc.cu",
-           "llattn_decode.cu", "llattn_bwd.cu", "llattn_bwd_tc.cu", "llattn_gdn.cu"]
+           "llattn_decode.cu", "llattn_bwd.cu", "llattn_bwd_tc.cu", "llattn_gdn.cu",
+           "llattn_qknorm.cu", "llattn_glr.cu", "llattn_decode_q8.cu"]
 HEADERS = ["llattn_internal.h", "llattn_common.cuh", "llattn_tc_ptx.cuh", "llattn_decode.h",
-           "llattn_bwd.h", "llattn_gdn.h"]
+           "llattn_bwd.h", "llattn_gdn.h", "llattn_qknorm.h", "llattn_glr.h",
+           "llattn_decode_q8.h"]
+# Built without --use_fast_math: exp of gates near 0 and sines of far positions at full fp32
+# precision, infinities and denormal block exponents as IEEE has them.
+PRECISE = {"llattn_qknorm.cu", "llattn_glr.cu", "llattn_decode_q8.cu"}
 LIB = os.path.join(HERE, "libllattn.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
@@ -54,7 +59,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     objs = []
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
-        cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-c",
+        flags = [f for f in NVCC_FLAGS if not (src in PRECISE and f == "--use_fast_math")]
+        cmd = [nvcc(), *flags, "-I", os.path.join(ROOT, "include"), "-c",
                os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         log = os.path.join(BUILD_DIR, src + ".log")

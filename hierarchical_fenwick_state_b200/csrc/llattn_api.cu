@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 #include <vector>
@@ -10,8 +11,11 @@
 #include "../../include/llattn.h"
 #include "llattn_bwd.h"
 #include "llattn_decode.h"
+#include "llattn_decode_q8.h"
 #include "llattn_gdn.h"
+#include "llattn_glr.h"
 #include "llattn_internal.h"
+#include "llattn_qknorm.h"
 
 // Per-device status word: kernels OR LLATTN_DEV_* bits into it.
 __device__ unsigned int g_llattn_status;
@@ -184,6 +188,56 @@ llattn_status forward(int in_dtype, int path, int chunk, const void* q, const vo
                       ? llattn::simt_forward(p, chunk, ws, st)
                       : llattn::tc_forward(p, chunk, ws, st, path == LLATTN_PATH_TCGEN05_SERIAL);
   if (e != cudaSuccess) return cuda_fail(e);
+  return LLATTN_OK;
+}
+
+// Memory that a call touches: `rows` pieces of `width` bytes at `stride` bytes from one another.
+struct Extent {
+  const void* p;
+  size_t width, rows, stride;
+};
+Extent flat(const void* p, size_t bytes) { return {p, bytes, 1, bytes}; }
+
+bool overlap(const Extent& a, const Extent& b) {
+  if (!a.p || !b.p || !a.width || !b.width || !a.rows || !b.rows) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + (a.rows - 1) * a.stride + a.width;
+  const uintptr_t b1 = b0 + (b.rows - 1) * b.stride + b.width;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.rows > 1 && b.rows > 1 && a.stride == b.stride) {   // columns of one wider buffer
+    const size_t off = (b0 >= a0 ? b0 - a0 : a.stride - (a0 - b0) % a.stride) % a.stride;
+    return !(off >= a.width && off + b.width <= a.stride);
+  }
+  return true;
+}
+
+// No output may overlap an input or another output.
+bool outputs_clear(const Extent* in, int nin, const Extent* out, int nout) {
+  for (int o = 0; o < nout; ++o) {
+    for (int i = 0; i < nin; ++i)
+      if (overlap(out[o], in[i])) return false;
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o], out[i])) return false;
+  }
+  return true;
+}
+
+constexpr unsigned long long kMaxElements = 1ull << 40;
+
+// The checks that llattn_qk_norm_rope and its backward share.
+llattn_status qk_check(int in_dtype, long long N, int Gq, int Gk, int H, int d, int rot, int layout,
+                       int norm, float eps, long long q_stride, long long k_stride) {
+  if (in_dtype != LLATTN_F32 && in_dtype != LLATTN_BF16) return LLATTN_ERR_DTYPE;
+  if (N < 0 || H < 1 || H > 65535 || Gq < 1 || Gk < 1 || Gq > H || Gk > H || H % Gq || H % Gk)
+    return LLATTN_ERR_SHAPE;
+  if (!head_dim_ok(d) || rot < 0 || rot > d || rot % 8) return LLATTN_ERR_SHAPE;
+  if (layout != LLATTN_ROPE_HALF && layout != LLATTN_ROPE_INTERLEAVED) return LLATTN_ERR_ARG;
+  if (norm != LLATTN_NORM_L2 && norm != LLATTN_NORM_RMS) return LLATTN_ERR_ARG;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return LLATTN_ERR_ARG;
+  if (q_stride < (long long)Gq * d || k_stride < (long long)Gk * d) return LLATTN_ERR_SHAPE;
+  if (N > (long long)(kMaxElements / ((unsigned long long)H * d)) || q_stride > (1ll << 31) ||
+      k_stride > (1ll << 31))
+    return LLATTN_ERR_SHAPE;
   return LLATTN_OK;
 }
 
@@ -727,6 +781,239 @@ llattn_status llattn_bwd(int in_dtype, const void* q, const void* k, const void*
   const cudaError_t e = llattn::bwd(p, ws, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   return LLATTN_OK;
+}
+
+llattn_status llattn_qk_norm_rope(int in_dtype, const void* q, const void* k, long long q_stride,
+                                  long long k_stride, const float* wq, const float* wk,
+                                  const int* pos, const float* inv_freq, void* qo, void* ko,
+                                  long long N, int Gq, int Gk, int H, int d, int rot, int layout,
+                                  int norm, float eps, void* stream) {
+  llattn_status s = qk_check(in_dtype, N, Gq, Gk, H, d, rot, layout, norm, eps, q_stride, k_stride);
+  if (s != LLATTN_OK) return s;
+  if (N == 0) return LLATTN_OK;  // nothing to compute
+  if (!q || !k || !qo || !ko || (rot && (!pos || !inv_freq))) return LLATTN_ERR_ARG;
+  const size_t e = in_dtype == LLATTN_BF16 ? 2 : 4;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(qo, 16) || !aligned(ko, 16) ||
+      q_stride * e % 16 || k_stride * e % 16 || !aligned(wq, 4) || !aligned(wk, 4) ||
+      !aligned(pos, 4) || !aligned(inv_freq, 4))
+    return LLATTN_ERR_ALIGN;
+  const size_t n = (size_t)N, row = (size_t)d * e;
+  const Extent in[6] = {{q, Gq * row, n, q_stride * e}, {k, Gk * row, n, k_stride * e},
+                        flat(wq, d * 4), flat(wk, d * 4), flat(rot ? pos : nullptr, n * 4),
+                        flat(rot ? inv_freq : nullptr, rot / 2 * 4)};
+  const Extent out[2] = {flat(qo, n * H * row), flat(ko, n * H * row)};
+  if (!outputs_clear(in, 6, out, 2)) return LLATTN_ERR_ARG;
+  llattn::QkProblem p{};
+  p.in_dtype = in_dtype;
+  p.x[0] = q; p.x[1] = k;
+  p.xs[0] = q_stride; p.xs[1] = k_stride;
+  p.w[0] = wq; p.w[1] = wk;
+  p.pos = pos; p.inv_freq = inv_freq;
+  p.y[0] = qo; p.y[1] = ko;
+  p.N = N; p.G[0] = Gq; p.G[1] = Gk;
+  p.H = H; p.d = d; p.rot = rot; p.layout = layout; p.norm = norm; p.eps = eps;
+  const cudaError_t err = llattn::qk_forward(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
+}
+
+llattn_status llattn_qk_norm_rope_bwd_workspace_bytes(int d, int weights, size_t* bytes) {
+  if (!bytes) return LLATTN_ERR_ARG;
+  if (!head_dim_ok(d)) return LLATTN_ERR_SHAPE;
+  *bytes = llattn::qk_bwd_workspace_bytes(d, weights != 0);
+  return LLATTN_OK;
+}
+
+llattn_status llattn_qk_norm_rope_bwd(
+    int in_dtype, const void* q, const void* k, long long q_stride, long long k_stride,
+    const float* wq, const float* wk, const int* pos, const float* inv_freq, const float* dqo,
+    const float* dko, float* dq, float* dk, long long dq_stride, long long dk_stride, float* dwq,
+    float* dwk, long long N, int Gq, int Gk, int H, int d, int rot, int layout, int norm,
+    float eps, void* workspace, size_t workspace_bytes, void* stream) {
+  llattn_status s = qk_check(in_dtype, N, Gq, Gk, H, d, rot, layout, norm, eps, q_stride, k_stride);
+  if (s != LLATTN_OK) return s;
+  if (dq_stride < (long long)Gq * d || dk_stride < (long long)Gk * d || dq_stride > (1ll << 31) ||
+      dk_stride > (1ll << 31))
+    return LLATTN_ERR_SHAPE;
+  if ((dwq && !wq) || (dwk && !wk)) return LLATTN_ERR_ARG;
+  if (N > 0 && (!q || !k || !dqo || !dko || !dq || !dk || (rot && (!pos || !inv_freq))))
+    return LLATTN_ERR_ARG;
+  const size_t e = in_dtype == LLATTN_BF16 ? 2 : 4;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(dqo, 16) || !aligned(dko, 16) ||
+      !aligned(dq, 16) || !aligned(dk, 16) || q_stride * e % 16 || k_stride * e % 16 ||
+      dq_stride % 4 || dk_stride % 4 || !aligned(wq, 4) || !aligned(wk, 4) || !aligned(dwq, 4) ||
+      !aligned(dwk, 4) || !aligned(pos, 4) || !aligned(inv_freq, 4))
+    return LLATTN_ERR_ALIGN;
+  const size_t n = (size_t)N, row = (size_t)d * e;
+  const Extent in[8] = {{q, Gq * row, n, q_stride * e}, {k, Gk * row, n, k_stride * e},
+                        flat(wq, d * 4), flat(wk, d * 4), flat(rot ? pos : nullptr, n * 4),
+                        flat(rot ? inv_freq : nullptr, rot / 2 * 4),
+                        flat(dqo, n * H * d * 4), flat(dko, n * H * d * 4)};
+  const Extent out[4] = {{dq, (size_t)Gq * d * 4, n, (size_t)dq_stride * 4},
+                         {dk, (size_t)Gk * d * 4, n, (size_t)dk_stride * 4},
+                         flat(dwq, d * 4), flat(dwk, d * 4)};
+  if (!outputs_clear(in, 8, out, 4)) return LLATTN_ERR_ARG;
+  if (N == 0 && !dwq && !dwk) return LLATTN_OK;  // nothing to compute
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  if ((s = device_state(&ds, &dev)) != LLATTN_OK) return s;
+  const size_t need = llattn::qk_bwd_workspace_bytes(d, dwq || dwk);
+  void* ws = nullptr;
+  std::unique_lock<std::mutex> lock(g_mu, std::defer_lock);
+  if ((s = pick_workspace(ds, need, workspace, workspace_bytes, lock, &ws)) != LLATTN_OK) return s;
+  llattn::QkProblem p{};
+  p.in_dtype = in_dtype;
+  p.x[0] = q; p.x[1] = k;
+  p.xs[0] = q_stride; p.xs[1] = k_stride;
+  p.w[0] = wq; p.w[1] = wk;
+  p.pos = pos; p.inv_freq = inv_freq;
+  p.dy[0] = dqo; p.dy[1] = dko;
+  p.dx[0] = dq; p.dx[1] = dk;
+  p.dxs[0] = dq_stride; p.dxs[1] = dk_stride;
+  p.dw[0] = dwq; p.dw[1] = dwk;
+  p.N = N; p.G[0] = Gq; p.G[1] = Gk;
+  p.H = H; p.d = d; p.rot = rot; p.layout = layout; p.norm = norm; p.eps = eps;
+  const cudaError_t err = llattn::qk_backward(p, ws, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
+}
+
+llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float* log_a, const float* h0,
+                             float* h, float* h_last, int B, int T, int D, const int* cu_seqlens,
+                             void* stream) {
+  if (in_dtype != LLATTN_F32 && in_dtype != LLATTN_BF16) return LLATTN_ERR_DTYPE;
+  if (B < 0 || T < 0 || D < 0 || B > 65535 || D > 65535 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
+  if ((unsigned long long)B * T > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
+  if (B == 0 || D == 0 || (T == 0 && !h_last)) return LLATTN_OK;  // nothing to compute
+  if (T > 0 && (!x || !log_a || !h)) return LLATTN_ERR_ARG;
+  const size_t e = in_dtype == LLATTN_BF16 ? 2 : 4;
+  if (!aligned(x, e) || !aligned(log_a, 4) || !aligned(h0, 4) || !aligned(h, 4) ||
+      !aligned(h_last, 4) || !aligned(cu_seqlens, 4))
+    return LLATTN_ERR_ALIGN;
+  // packed: the host knows that the tensors hold a row at least, if T > 0
+  const size_t n = (cu_seqlens ? (T > 0) : (size_t)B * T) * D, st = (size_t)B * D * 4;
+  const Extent in[4] = {flat(x, n * e), flat(log_a, n * 4), flat(h0 == h_last ? nullptr : h0, st),
+                        flat(cu_seqlens, ((size_t)B + 1) * 4)};
+  const Extent out[2] = {flat(h, n * 4), flat(h_last, st)};
+  if (!outputs_clear(in, 4, out, 2)) return LLATTN_ERR_ARG;
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  llattn_status s = device_state(&ds, &dev);
+  if (s != LLATTN_OK) return s;
+  llattn::GlrProblem p{in_dtype, x, log_a, h0, h, h_last, B, T, D, cu_seqlens, ds->status};
+  const cudaError_t err = llattn::glr_forward(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
+}
+
+llattn_status llattn_glr_bwd(const float* log_a, const float* h, const float* h0, const float* dh,
+                             const float* dh_last, float* dx, float* dlog_a, float* dh0, int B,
+                             int T, int D, const int* cu_seqlens, void* stream) {
+  if (B < 0 || T < 0 || D < 0 || B > 65535 || D > 65535 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
+  if ((unsigned long long)B * T > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
+  if (B == 0 || D == 0 || (T == 0 && !dh0)) return LLATTN_OK;  // nothing to compute
+  if (T > 0 && (!log_a || !h || !dh || !dx || !dlog_a)) return LLATTN_ERR_ARG;
+  const void* ptrs[9] = {log_a, h, h0, dh, dh_last, dx, dlog_a, dh0, cu_seqlens};
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return LLATTN_ERR_ALIGN;
+  const size_t n = (cu_seqlens ? (T > 0) : (size_t)B * T) * D * 4, st = (size_t)B * D * 4;
+  const Extent in[6] = {flat(log_a, n), flat(h, n), flat(h0, st), flat(dh, n), flat(dh_last, st),
+                        flat(cu_seqlens, ((size_t)B + 1) * 4)};
+  const Extent out[3] = {flat(dx, n), flat(dlog_a, n), flat(dh0, st)};
+  if (!outputs_clear(in, 6, out, 3)) return LLATTN_ERR_ARG;
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  llattn_status s = device_state(&ds, &dev);
+  if (s != LLATTN_OK) return s;
+  llattn::GlrBwdProblem p{log_a, h, h0, dh, dh_last, dx, dlog_a, dh0, B, T, D, cu_seqlens,
+                          ds->status};
+  const cudaError_t err = llattn::glr_backward(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
+}
+
+llattn_status llattn_decode_q8_state_bytes(int B, int H, int L, int dk, int dv, size_t* bytes) {
+  if (!bytes) return LLATTN_ERR_ARG;
+  if (B < 0 || H < 0 || B > 65535 || H > 65535 || L < 1 || L > 32) return LLATTN_ERR_SHAPE;
+  if (!head_dim_ok(dk) || !head_dim_ok(dv)) return LLATTN_ERR_SHAPE;
+  *bytes = llattn::q8_state_bytes(B, H, L, dk, dv);
+  return LLATTN_OK;
+}
+
+llattn_status llattn_decode_step_q8(int in_dtype, const void* q, const void* k, const void* v,
+                                    const float* log_a, const float* lam, const int* pos,
+                                    void* state, float* out, int B, int H, int L, int dk, int dv,
+                                    void* stream) {
+  if (in_dtype != LLATTN_F32 && in_dtype != LLATTN_BF16) return LLATTN_ERR_DTYPE;
+  size_t state_bytes = 0;
+  llattn_status s = llattn_decode_q8_state_bytes(B, H, L, dk, dv, &state_bytes);
+  if (s != LLATTN_OK) return s;
+  if (B == 0 || H == 0) return LLATTN_OK;  // nothing to compute
+  if (!q || !k || !v || !log_a || !lam || !pos || !state || !out) return LLATTN_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(state, 16) ||
+      !aligned(out, 16) || !aligned(log_a, 4) || !aligned(lam, 4) || !aligned(pos, 4))
+    return LLATTN_ERR_ALIGN;
+  const size_t bh = (size_t)B * H, e = in_dtype == LLATTN_BF16 ? 2 : 4;
+  const Extent in[6] = {flat(q, bh * dk * e), flat(k, bh * dk * e), flat(v, bh * dv * e),
+                        flat(log_a, bh * 4), flat(lam, bh * L * 4), flat(pos, (size_t)B * 4)};
+  const Extent outs[2] = {flat(state, state_bytes), flat(out, bh * dv * 4)};
+  if (!outputs_clear(in, 6, outs, 2)) return LLATTN_ERR_ARG;
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  if ((s = device_state(&ds, &dev)) != LLATTN_OK) return s;
+  llattn::Q8StepProblem p{in_dtype, q, k, v, log_a, lam, pos,
+                          llattn::q8_state_views(state, B, H, L, dk, dv), out, B, H, L, dk, dv,
+                          ds->status};
+  const cudaError_t err = llattn::q8_step(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
+}
+
+llattn_status llattn_prefill_state_q8(int in_dtype, const void* k, const void* v,
+                                      const float* log_a, void* state, int B, int H, int T, int L,
+                                      int dk, int dv, const int* cu_seqlens, void* stream) {
+  if (in_dtype != LLATTN_F32 && in_dtype != LLATTN_BF16) return LLATTN_ERR_DTYPE;
+  size_t state_bytes = 0;
+  llattn_status s = llattn_decode_q8_state_bytes(B, H, L, dk, dv, &state_bytes);
+  if (s != LLATTN_OK) return s;
+  if (T < 0 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
+  if (B == 0 || H == 0) return LLATTN_OK;  // nothing to compute
+  if (!state) return LLATTN_ERR_ARG;
+  if (T > 0 && (!k || !v || !log_a)) return LLATTN_ERR_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(state, 16) || !aligned(log_a, 4) ||
+      !aligned(cu_seqlens, 4))
+    return LLATTN_ERR_ALIGN;
+  // packed: the host knows that the tensors hold a row at least, if T > 0
+  const size_t rows = (cu_seqlens ? (T > 0) : (size_t)B * T) * H, e = in_dtype == LLATTN_BF16 ? 2 : 4;
+  const Extent in[4] = {flat(k, rows * dk * e), flat(v, rows * dv * e), flat(log_a, rows * 4),
+                        flat(cu_seqlens, ((size_t)B + 1) * 4)};
+  const Extent out = flat(state, state_bytes);
+  if (!outputs_clear(in, 4, &out, 1)) return LLATTN_ERR_ARG;
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  if ((s = device_state(&ds, &dev)) != LLATTN_OK) return s;
+  llattn::Q8PrefillProblem p{in_dtype, k, v, log_a, llattn::q8_state_views(state, B, H, L, dk, dv),
+                             B, H, T, L, dk, dv, cu_seqlens, ds->status};
+  const cudaError_t err = llattn::q8_prefill(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
+}
+
+llattn_status llattn_read_state_q8(const void* state, const int* slot, void* out, int out_dtype,
+                                   int B, int H, int L, int dk, int dv, void* stream) {
+  if (out_dtype != LLATTN_F32 && out_dtype != LLATTN_BF16) return LLATTN_ERR_DTYPE;
+  size_t state_bytes = 0;
+  llattn_status s = llattn_decode_q8_state_bytes(B, H, L, dk, dv, &state_bytes);
+  if (s != LLATTN_OK) return s;
+  if (B == 0 || H == 0 || L == 1) return LLATTN_OK;  // no slots
+  if (!state || !out) return LLATTN_ERR_ARG;
+  if (!aligned(state, 16) || !aligned(out, 16) || !aligned(slot, 4)) return LLATTN_ERR_ALIGN;
+  const size_t slots = (size_t)B * H * (slot ? 1 : (size_t)(L - 1));
+  const Extent in[2] = {flat(state, state_bytes), flat(slot, (size_t)B * 4)};
+  const Extent o = flat(out, slots * dk * dv * (out_dtype == LLATTN_BF16 ? 2 : 4));
+  if (!outputs_clear(in, 2, &o, 1)) return LLATTN_ERR_ARG;
+  DeviceState* ds = nullptr;
+  int dev = 0;
+  if ((s = device_state(&ds, &dev)) != LLATTN_OK) return s;
+  // the views of a const buffer: llattn::q8_read writes only `out`
+  llattn::Q8ReadProblem p{llattn::q8_state_views(const_cast<void*>(state), B, H, L, dk, dv), slot,
+                          out, out_dtype, B, H, L, dk, dv, ds->status};
+  const cudaError_t err = llattn::q8_read(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
 }
 
 int llattn_last_cuda_error(void) { return t_last_cuda; }

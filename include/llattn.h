@@ -442,6 +442,144 @@ LLATTN_API llattn_status llattn_gdn_fwd(int in_dtype, const void* q, const void*
                                         int dv, const int* cu_seqlens, void* stream);
 
 /*
+ * llattn_qk_norm_rope - norms of queries and keys for each head, with the position rotation in
+ * the same pass: turns a projection's output into the q, k that llattn_fwd, llattn_bwd and the
+ * decoding steps take (the tensor-core forward wants rows of unit norm).  A row x is the d values
+ * of one token and one head, or of one group of heads that share it:
+ *
+ *   u = x * inv,  inv = (sum x^2 + eps)^(-1/2)  (LLATTN_NORM_L2)  or  (sum x^2 / d + eps)^(-1/2)
+ *   (LLATTN_NORM_RMS);   y = R (u * w),
+ *   R turns the pairs of the first rot values by the angle pos * inv_freq[pair]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos), a pair being values (i, i + rot/2) for
+ *   LLATTN_ROPE_HALF, (2i, 2i + 1) for LLATTN_ROPE_INTERLEAVED; the other d - rot values pass.
+ *
+ *   in_dtype   LLATTN_BF16 or LLATTN_F32: the type of q, k and of qo, ko.  Arithmetic is fp32,
+ *              angles are formed in fp64, outputs are rounded once.
+ *   q, k       N tokens of Gq (Gk) rows of d values, the rows of a token side by side; token t
+ *              starts at q + t * q_stride (k + t * k_stride), strides in elements, so that both
+ *              may lie in one projection's output.
+ *   wq, wk     fp32 [d], the norm's weights (shared by the heads), or NULL for 1.
+ *   pos        DEVICE int32 [N], each token's position (any value; llattn_decode_step's pos for
+ *              a step); inv_freq fp32 [rot/2], applied as given (the caller scales it for long
+ *              contexts).  Both may be NULL when rot = 0.
+ *   qo, ko     [N, H, d]: row g is written to heads g*H/Gq .. (g+1)*H/Gq - 1 (Gk for keys).
+ *   d          in {32, 64, 128}; rot a multiple of 8, 0 <= rot <= d; H a multiple of Gq and of
+ *              Gk, all at most 65535; eps > 0 and finite; strides at least G*d.
+ * Pointers q, k, qo, ko 16-byte aligned and strides a multiple of 16 bytes, the rest 4-byte
+ * aligned; no output may overlap an input or the other output.  No scratch memory.
+ * Asynchronous on `stream`.  A row that holds an infinity or NaN gives NaN in that row alone.
+ */
+enum { LLATTN_NORM_L2 = 0, LLATTN_NORM_RMS = 1 };
+enum { LLATTN_ROPE_HALF = 0, LLATTN_ROPE_INTERLEAVED = 1 };
+LLATTN_API llattn_status llattn_qk_norm_rope(int in_dtype, const void* q, const void* k,
+                                             long long q_stride, long long k_stride,
+                                             const float* wq, const float* wk, const int* pos,
+                                             const float* inv_freq, void* qo, void* ko,
+                                             long long N, int Gq, int Gk, int H, int d, int rot,
+                                             int layout, int norm, float eps, void* stream);
+
+/*
+ * llattn_qk_norm_rope_bwd - its gradients, from those at qo and ko.  With z = R^T (sum of the
+ * gradients of the heads that share the row) and t = <z w, u> (/ d for LLATTN_NORM_RMS):
+ *   dx = inv (z w - u t),   dw = sum over all rows of z u.
+ *   dqo, dko   fp32 [N, H, d] (what llattn_bwd writes as dq, dk).
+ *   dq, dk     fp32, N tokens of Gq (Gk) rows of d at strides dq_stride, dk_stride (elements):
+ *              fully overwritten, nothing between the rows is touched; the two may lie side by
+ *              side in one buffer of equal strides.
+ *   dwq, dwk   fp32 [d] or NULL (not computed); non-NULL only where wq (wk) is.
+ *   workspace  caller-owned device scratch of llattn_qk_norm_rope_bwd_workspace_bytes() bytes
+ *              (256-byte aligned), or NULL for the library's per-device buffer (as llattn_fwd);
+ *              needed for dwq, dwk alone.  Sums run in a fixed order: the same call gives the
+ *              same bits.
+ * The rest as llattn_qk_norm_rope.
+ */
+LLATTN_API llattn_status llattn_qk_norm_rope_bwd_workspace_bytes(int d, int weights,
+                                                                 size_t* bytes);
+LLATTN_API llattn_status llattn_qk_norm_rope_bwd(
+    int in_dtype, const void* q, const void* k, long long q_stride, long long k_stride,
+    const float* wq, const float* wk, const int* pos, const float* inv_freq, const float* dqo,
+    const float* dko, float* dq, float* dk, long long dq_stride, long long dk_stride, float* dwq,
+    float* dwk, long long N, int Gq, int Gk, int H, int d, int rot, int layout, int norm,
+    float eps, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * llattn_glr_fwd - the gated linear recurrence over a dense or packed batch, each of D channels
+ * on its own, in fp32:
+ *
+ *   h_t = exp(log_a_t) h_{t-1} + x_t,   h_{-1} = h0.
+ *
+ *   in_dtype   LLATTN_BF16 or LLATTN_F32: the type of x.
+ *   x          [B, T, D] (packed: [total, D]); log_a the same shape, fp32, any sign; -inf starts
+ *              a channel afresh at that token.
+ *   h0         fp32 [B, D], the state carried in, or NULL for 0.
+ *   h          fp32 [.., D], fully overwritten for every token of every sequence (a packed
+ *              sequence longer than T is cut at T, as in llattn_fwd; other rows are untouched).
+ *   h_last     fp32 [B, D] or NULL: the state after the last token (h0 or 0 for an empty
+ *              sequence).  May be h0 itself: a decoding step is T = 1 with one state buffer.
+ *   cu_seqlens as in llattn_fwd.  B, D <= 65535, 0 <= T <= 2^24.
+ * Pointers aligned to their type (16-byte alignment and D a multiple of 8 run fastest); no
+ * output may overlap an input or another output, h_last == h0 excepted.  No scratch memory.
+ * Asynchronous on `stream`.
+ */
+LLATTN_API llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float* log_a,
+                                        const float* h0, float* h, float* h_last, int B, int T,
+                                        int D, const int* cu_seqlens, void* stream);
+
+/*
+ * llattn_glr_bwd - its gradients from dh (at h) and dh_last (at h_last), with h as llattn_glr_fwd
+ * gave it:
+ *   g_t = dh_t + exp(log_a_{t+1}) g_{t+1}  (+ dh_last at the last token),
+ *   dx_t = g_t,   dlog_a_t = g_t exp(log_a_t) h_{t-1},   dh0 = exp(log_a_0) g_0.
+ *   log_a, h, dh   fp32 [.., D]; h0, dh_last fp32 [B, D] or NULL for 0.
+ *   dx, dlog_a     fp32 [.., D], fully overwritten as h is in llattn_glr_fwd.
+ *   dh0            fp32 [B, D] or NULL (not computed); dh_last for an empty sequence.
+ * The rest as llattn_glr_fwd; no output may overlap an input or another output.
+ */
+LLATTN_API llattn_status llattn_glr_bwd(const float* log_a, const float* h, const float* h0,
+                                        const float* dh, const float* dh_last, float* dx,
+                                        float* dlog_a, float* dh0, int B, int T, int D,
+                                        const int* cu_seqlens, void* stream);
+
+/*
+ * The decoding state in 8 bits: a quarter of llattn_decode_step's state and of the bytes that a
+ * step reads, for decoding batches whose state fills the memory.
+ *
+ * A slot's dk x dv state is held as whole numbers in -127..127 times a power of two for every 32
+ * adjacent values of a row: the smallest 2^e with max |x| <= 127 * 2^e, x / 2^e rounded to the
+ * nearest (ties to even).  A value is rounded when its level is carried, so each token's
+ * contribution at most log2(T) times, by at most 1/254 of the block's largest value (twice that
+ * just above a power of two).
+ *
+ * llattn_decode_q8_state_bytes - size of the state buffer.  Layout: codes int8
+ *   [B, H, L-1, dk, dv] (slot j = level j+1), then gate fp32 [B, H, 2, L-1] with the meaning it
+ *   has in llattn_decode_step, then exps uint8 [B, H, L-1, dk, dv/32]: e + 127, 0 for a block of
+ *   zeros, 255 for one that was to hold an infinity or NaN (it reads as NaN).
+ * llattn_decode_step_q8 - llattn_decode_step on such a state; arguments as there.
+ * llattn_prefill_state_q8 - llattn_prefill_state on such a state; arguments as there.  The sums
+ *   over a bucket are accumulated in fp32.
+ * llattn_read_state_q8 - the held values, as slots store them (their pending gates not applied),
+ *   exactly for both types: slot NULL gives every slot, out [B, H, L-1, dk, dv] (slots that hold
+ *   no level read as whatever they last held); a DEVICE int32 array slot [B] gives slot slot[b]
+ *   of each sequence, out [B, H, dk, dv] (an index outside [0, L-1) leaves that sequence's rows
+ *   untouched and sets LLATTN_DEV_DECODE_POS).  out_dtype LLATTN_F32 or LLATTN_BF16.
+ * State and out 16-byte aligned, slot 4-byte; out must not overlap the state.
+ */
+LLATTN_API llattn_status llattn_decode_q8_state_bytes(int B, int H, int L, int dk, int dv,
+                                                      size_t* bytes);
+LLATTN_API llattn_status llattn_decode_step_q8(int in_dtype, const void* q, const void* k,
+                                               const void* v, const float* log_a,
+                                               const float* lam, const int* pos, void* state,
+                                               float* out, int B, int H, int L, int dk, int dv,
+                                               void* stream);
+LLATTN_API llattn_status llattn_prefill_state_q8(int in_dtype, const void* k, const void* v,
+                                                 const float* log_a, void* state, int B, int H,
+                                                 int T, int L, int dk, int dv,
+                                                 const int* cu_seqlens, void* stream);
+LLATTN_API llattn_status llattn_read_state_q8(const void* state, const int* slot, void* out,
+                                              int out_dtype, int B, int H, int L, int dk, int dv,
+                                              void* stream);
+
+/*
  * Launch accounting, for benchmarks.  llattn_profile(1) starts recording a pair
  * of CUDA events on the call's stream around the dominant kernel of every
  * forward (the one that streams q, k, v, lam and writes out); llattn_profile(0)
