@@ -28,7 +28,7 @@ EXPORTS = (
     "llattn_bwd_workspace_bytes", "llattn_bwd", "llattn_fwd_bf16", "llattn_stream_status",
     "llattn_segment_plan", "llattn_set_segment_chunks", "llattn_gdn_fwd",
     "llattn_prefill_state", "llattn_qk_norm_rope", "llattn_qk_norm_rope_bwd_workspace_bytes",
-    "llattn_qk_norm_rope_bwd", "llattn_glr_fwd", "llattn_glr_bwd",
+    "llattn_qk_norm_rope_bwd", "llattn_glr_workspace_bytes", "llattn_glr_fwd", "llattn_glr_bwd",
     "llattn_decode_q8_state_bytes", "llattn_decode_step_q8", "llattn_prefill_state_q8",
     "llattn_read_state_q8",
 )
@@ -108,10 +108,12 @@ def lib():
     L.llattn_qk_norm_rope_bwd.restype = i
     L.llattn_qk_norm_rope_bwd.argtypes = [i, vp, vp, ll, ll, f_p, f_p, i_p, f_p, f_p, f_p, f_p, f_p,
                                           ll, ll, f_p, f_p, ll, i, i, i, i, i, i, i, fl, vp, sz, vp]
+    L.llattn_glr_workspace_bytes.restype = i
+    L.llattn_glr_workspace_bytes.argtypes = [i, i, i, szp]
     L.llattn_glr_fwd.restype = i
-    L.llattn_glr_fwd.argtypes = [i, vp, f_p, f_p, f_p, f_p, i, i, i, i_p, vp]
+    L.llattn_glr_fwd.argtypes = [i, vp, f_p, f_p, f_p, f_p, i, i, i, i_p, vp, sz, vp]
     L.llattn_glr_bwd.restype = i
-    L.llattn_glr_bwd.argtypes = [f_p] * 8 + [i, i, i, i_p, vp]
+    L.llattn_glr_bwd.argtypes = [f_p] * 8 + [i, i, i, i_p, vp, sz, vp]
     L.llattn_decode_q8_state_bytes.restype = i
     L.llattn_decode_q8_state_bytes.argtypes = [i, i, i, i, i, szp]
     L.llattn_decode_step_q8.restype = i
@@ -431,14 +433,16 @@ def stream_status(clear: bool = True, stream=None) -> int:
 def _on_device(fn, dev, stream, where, args):
     """The C call `fn(*args, stream)` with `dev`, the tensors' device, current."""
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+    C = torch._C
+    # torch.cuda.current_stream() builds a Stream object (4 us of a 10 us call); its raw handle will do
+    raw = stream.cuda_stream if stream is not None else C._cuda_getCurrentRawStream(dev.index)
+    if dev.index == C._cuda_getDevice():
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
-    _check(st, where)
+            st = fn(*args, raw)
+    if st != 0:
+        raise LLAttnError(st, where)
 
 
 def _ptr(t):
@@ -610,8 +614,30 @@ def _glr_shape(t, cu_seqlens, T):
     return B, T, rest.numel(), (B,) + tuple(rest)
 
 
+def glr_workspace_bytes(B: int, T: int, D: int) -> int:
+    """Bytes of scratch of glr_forward and of glr_backward (llattn_glr_workspace_bytes)."""
+    n = ctypes.c_size_t(0)
+    _check(lib().llattn_glr_workspace_bytes(int(B), int(T), int(D), ctypes.byref(n)),
+           "llattn_glr_workspace_bytes")
+    return int(n.value)
+
+
+def _glr_workspace(workspace, B, T, D, dev, stream):
+    """The call's scratch: the caller's, or torch's for this call alone (none where none is needed)."""
+    import torch
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    n = glr_workspace_bytes(B, T, D)
+    if n == 0:
+        return None, 0
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev), n
+    with torch.cuda.stream(stream):   # torch hands it on in that stream's order
+        return torch.empty(n, dtype=torch.uint8, device=dev), n
+
+
 def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[int] = None,
-                out=None, stream=None):
+                out=None, workspace=None, stream=None):
     """The gated linear recurrence h_t = exp(log_a_t) h_{t-1} + x_t (llattn_glr_fwd): returns h (fp32).
 
     x bf16 or fp32 and log_a fp32, both [B, T, ...channels], or [total, ...channels] with
@@ -631,14 +657,15 @@ def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[
         out = torch.empty(x.shape, dtype=f32, device=dev)
     else:
         _expect(out, "out", f32, x.shape, dev)
+    ws, ws_n = _glr_workspace(workspace, B, T, D, dev, stream)
     _on_device(lib().llattn_glr_fwd, dev, stream, "llattn_glr_fwd",
                (dt, _ptr(x), _ptr(log_a), _ptr(h0), _ptr(out), _ptr(h_last), B, T, D,
-                _ptr(cu_seqlens)))
+                _ptr(cu_seqlens), _ptr(ws), ws_n))
     return out
 
 
 def glr_backward(log_a, h, dh, *, h0=None, dh_last=None, cu_seqlens=None, T: Optional[int] = None,
-                 grads=None, stream=None):
+                 grads=None, workspace=None, stream=None):
     """Gradients of glr_forward from dh (and dh_last) through llattn_glr_bwd.
 
     log_a, h (the forward's output), dh fp32, shaped as in the forward; h0, dh_last fp32
@@ -666,9 +693,11 @@ def glr_backward(log_a, h, dh, *, h0=None, dh_last=None, cu_seqlens=None, T: Opt
         _expect(t, "grads['h0']", f32, None, dev)
         if t is not None and t.numel() != B * D:
             raise ValueError(f"grads['h0'] must have shape {state}")
+    ws, ws_n = _glr_workspace(workspace, B, T, D, dev, stream)
     _on_device(lib().llattn_glr_bwd, dev, stream, "llattn_glr_bwd",
                (_ptr(log_a), _ptr(h), _ptr(h0), _ptr(dh), _ptr(dh_last), _ptr(grads["x"]),
-                _ptr(grads["log_a"]), _ptr(grads.get("h0")), B, T, D, _ptr(cu_seqlens)))
+                _ptr(grads["log_a"]), _ptr(grads.get("h0")), B, T, D, _ptr(cu_seqlens), _ptr(ws),
+                ws_n))
     return grads
 
 
@@ -683,7 +712,7 @@ def decode_q8_state_bytes(B: int, H: int, L: int, dk: int, dv: int) -> int:
 def _q8_state(state, B, H, L, dk, dv):
     if not state.is_cuda or not state.is_contiguous():
         raise ValueError("state must be a contiguous CUDA tensor")
-    need = decode_q8_state_bytes(B, H, L, dk, dv)
+    need = B * H * (L - 1) * (dk * dv + 8 + dk * (dv // 32))   # as llattn_decode_q8_state_bytes
     if state.numel() * state.element_size() < need:
         raise ValueError(f"state must hold {need} bytes")
     return state.device

@@ -876,9 +876,17 @@ llattn_status llattn_qk_norm_rope_bwd(
   return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
 }
 
+llattn_status llattn_glr_workspace_bytes(int B, int T, int D, size_t* bytes) {
+  if (!bytes) return LLATTN_ERR_ARG;
+  if (B < 0 || T < 0 || D < 0 || B > 65535 || D > 65535 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
+  if ((unsigned long long)B * T > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
+  *bytes = B == 0 || D == 0 ? 0 : llattn::glr_workspace_bytes(B, T, D);
+  return LLATTN_OK;
+}
+
 llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float* log_a, const float* h0,
                              float* h, float* h_last, int B, int T, int D, const int* cu_seqlens,
-                             void* stream) {
+                             void* workspace, size_t workspace_bytes, void* stream) {
   if (in_dtype != LLATTN_F32 && in_dtype != LLATTN_BF16) return LLATTN_ERR_DTYPE;
   if (B < 0 || T < 0 || D < 0 || B > 65535 || D > 65535 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
   if ((unsigned long long)B * T > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
@@ -898,14 +906,20 @@ llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float* log_a, co
   int dev = 0;
   llattn_status s = device_state(&ds, &dev);
   if (s != LLATTN_OK) return s;
+  void* ws = nullptr;
+  std::unique_lock<std::mutex> lock(g_mu, std::defer_lock);
+  if ((s = pick_workspace(ds, llattn::glr_workspace_bytes(B, T, D), workspace, workspace_bytes, lock,
+                          &ws)) != LLATTN_OK)
+    return s;
   llattn::GlrProblem p{in_dtype, x, log_a, h0, h, h_last, B, T, D, cu_seqlens, ds->status};
-  const cudaError_t err = llattn::glr_forward(p, static_cast<cudaStream_t>(stream));
+  const cudaError_t err = llattn::glr_forward(p, ws, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
 }
 
 llattn_status llattn_glr_bwd(const float* log_a, const float* h, const float* h0, const float* dh,
                              const float* dh_last, float* dx, float* dlog_a, float* dh0, int B,
-                             int T, int D, const int* cu_seqlens, void* stream) {
+                             int T, int D, const int* cu_seqlens, void* workspace,
+                             size_t workspace_bytes, void* stream) {
   if (B < 0 || T < 0 || D < 0 || B > 65535 || D > 65535 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
   if ((unsigned long long)B * T > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
   if (B == 0 || D == 0 || (T == 0 && !dh0)) return LLATTN_OK;  // nothing to compute
@@ -922,9 +936,14 @@ llattn_status llattn_glr_bwd(const float* log_a, const float* h, const float* h0
   int dev = 0;
   llattn_status s = device_state(&ds, &dev);
   if (s != LLATTN_OK) return s;
+  void* ws = nullptr;
+  std::unique_lock<std::mutex> lock(g_mu, std::defer_lock);
+  if ((s = pick_workspace(ds, llattn::glr_workspace_bytes(B, T, D), workspace, workspace_bytes, lock,
+                          &ws)) != LLATTN_OK)
+    return s;
   llattn::GlrBwdProblem p{log_a, h, h0, dh, dh_last, dx, dlog_a, dh0, B, T, D, cu_seqlens,
                           ds->status};
-  const cudaError_t err = llattn::glr_backward(p, static_cast<cudaStream_t>(stream));
+  const cudaError_t err = llattn::glr_backward(p, ws, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
 }
 

@@ -8,25 +8,498 @@
 //   dx_t = g_t,   dlog_a_t = g_t a_t h_{t-1},   dh0 = a_0 g_0.
 //
 // A gate of log_a = -inf (a = 0) starts the channel afresh at that token.
+//
+// Tiles.  n steps of a channel are the map y -> P y + H with P the product of their gates and H
+// the state they reach from 0, and maps of adjacent steps join as (P2 P1, P2 H1 + H2).  A CTA
+// takes tiles of 32 channels and TT steps: each thread walks S steps of its channels, copied to
+// its own places of shared memory, to their map; the threads' maps join over the warp (shuffles)
+// and the CTA (shared memory); the state that enters the tile comes from the tiles before it, and
+// a second walk writes the outputs.  So every input is read once and every output written once,
+// and tiles of one long sequence fill the machine as those of many short ones do.
+//
+// What bounds it: memory traffic (10 bytes per element forward with bf16 x, 20 backward), as long
+// as enough CTAs are resident to hide a tile's chain of copy, join, look-back and store.  Three
+// CTAs of 256 threads with one tile each in flight carry 134 M elements in 262 us as one sequence
+// of 65536 steps and in 239 us as eight (5.1 and 5.6 TB/s); two CTAs with the next tile copied
+// ahead took 289 and 284 us, tiles held in registers 300 and 288, and clusters of eight CTAs that
+// walk a sequence side by side and pass the state through distributed shared memory 285 and 298:
+// they leave SMs idle at every shape that is no multiple of their waves.  With 32 channels a row
+// of a tile is one 128-byte line of log_a; 64 and 128 channels made fewer and larger tiles and no
+// better use of memory.
+//
+// Look-back.  A tile publishes its map (32 channels: one 16-byte record each, written and read
+// whole, so no fence is needed) before it knows what enters it.  Tiles are grouped by eight in
+// time: what enters tile k is the state that the last tile of the group before (in the first
+// group: the sequence's first tile) has published, carried through the maps of the group's earlier tiles in their order.  The grouping is fixed,
+// so the rounding is too: the same call gives the same bits, whichever tiles happen to be ready.
+// Tiles are handed out by a counter in an order in which a tile comes after all that it looks
+// back at, so those run or have run, and every wait ends (and is bounded all the same).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/llattn.h"
 #include "llattn_common.cuh"
 #include "llattn_glr.h"
 #include "llattn_internal.h"
+#include "llattn_tc_ptx.cuh"
 
 namespace llattn {
 namespace {
 
-constexpr int kGlrThreads = 128;
+constexpr int kCT = 32;          // channels per tile
+constexpr int kGroup = 8;        // tiles whose maps are joined one by one
 
-// One thread per (sequence, channel), token by token.
+// ---- values on their way through shared memory: VEC channels of one step ----
+template <int VEC>
+struct alignas(4 * VEC) Floats {
+  float v[VEC];
+};
+// x as it lies in memory.  A lone bf16 cannot be copied asynchronously (4 bytes at least): the
+// aligned word around it is, and `odd` says which half it is.
+template <typename T, int VEC>
+struct Raw;
+template <int VEC>
+struct alignas(4 * VEC) Raw<float, VEC> {
+  float v[VEC];
+  __device__ __forceinline__ float get(int i, unsigned) const { return v[i]; }
+};
+template <>
+struct alignas(8) Raw<__nv_bfloat16, 4> {
+  unsigned w[2];
+  __device__ __forceinline__ float get(int i, unsigned) const {
+    return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+  }
+};
+template <>
+struct alignas(4) Raw<__nv_bfloat16, 1> {
+  unsigned w;
+  __device__ __forceinline__ float get(int, unsigned odd) const {
+    return __uint_as_float(odd ? (w & 0xffff0000u) : (w << 16));
+  }
+};
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+template <int VEC>
+__device__ __forceinline__ void copy_x(Raw<float, VEC>* dst, const float* src) { cp_async<4 * VEC>(dst, src); }
+__device__ __forceinline__ void copy_x(Raw<__nv_bfloat16, 4>* dst, const __nv_bfloat16* src) { cp_async<8>(dst, src); }
+__device__ __forceinline__ void copy_x(Raw<__nv_bfloat16, 1>* dst, const __nv_bfloat16* src) {
+  cp_async<4>(dst, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)3));
+}
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// exp(x) as 2^(x log2 e): two instructions in place of nine.  Off by the rounding of the product
+// and of log2 e, 1.25 |x| 2^-24 relative, and two steps: what matters is a's own size, and |x| e^x
+// is below 0.37.  -inf gives 0, NaN stays.
+__device__ __forceinline__ float gate(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+
+template <int VEC>
+__device__ __forceinline__ void st_vec(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 4) __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+  else __stcs(p, v[0]);
+}
+
+// What a tile has published of one channel: its map, and with kDone the state that leaves it.
+enum : unsigned { kNothing = 0u, kMap = 1u, kDone = 2u };
+struct alignas(16) Record {
+  float P, H, out;
+  unsigned what;
+};
+
+__device__ __forceinline__ void publish(Record* r, float P, float H, float out, unsigned what) {
+  const uint64_t lo = (uint64_t)__float_as_uint(P) | ((uint64_t)__float_as_uint(H) << 32);
+  const uint64_t hi = (uint64_t)__float_as_uint(out) | ((uint64_t)what << 32);
+  asm volatile("{\n\t.reg .b128 q;\n\tmov.b128 q, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], q;\n\t}"
+               ::"l"(r), "l"(lo), "l"(hi) : "memory");
+}
+__device__ __forceinline__ Record look(const Record* r) {
+  uint64_t lo, hi;
+  asm volatile("{\n\t.reg .b128 q;\n\tld.relaxed.gpu.global.b128 q, [%2];\n\tmov.b128 {%0, %1}, q;\n\t}"
+               : "=l"(lo), "=l"(hi) : "l"(r) : "memory");
+  return {__uint_as_float((unsigned)lo), __uint_as_float((unsigned)(lo >> 32)),
+          __uint_as_float((unsigned)hi), (unsigned)(hi >> 32)};
+}
+
+// The record (x at the last look) once it holds `what` or more; a zero record and a status bit if
+// it never does.
+__device__ __forceinline__ Record wait_for(Record x, const Record* r, unsigned what, unsigned int* status) {
+  if (x.what >= what) return x;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (;;) {
+    for (int i = 0; i < 32; ++i) {
+      x = look(r);
+      if (x.what >= what) return x;
+    }
+    if (ptx::globaltimer_ns() - t0 > 2000000000ull) {
+      atomicOr(status, LLATTN_DEV_WAIT_TIMEOUT);
+      return {0.f, 0.f, 0.f, what};
+    }
+  }
+}
+
+// The scratch of a call: the counter that hands out tiles, then the records, by (time tile,
+// sequence, channel tile, channel).  Zeroed before the kernel.
+struct Scratch {
+  unsigned* next;
+  Record* rec;
+};
+constexpr size_t kScratchHead = 256;
+
+// A tile: time tile k of sequence b, 32 channels from ct * 32; the sequence's first row and length.
+// k < 0: no more tiles.
+struct Job {
+  int k, b, ct, len;
+  long long start;
+};
+
+template <int TT>
+__device__ __forceinline__ Job take_job(unsigned* next, unsigned& turn, unsigned total, int nseq,
+                                        int cts, int T, const int* cu, unsigned int* status) {
+  const unsigned per = (unsigned)nseq * cts;
+  for (;;) {
+    unsigned i;
+    if (next) {
+      i = atomicAdd(next, 1u);
+    } else {   // one tile in time for each sequence: no order to keep
+      i = turn;
+      turn += gridDim.x;
+    }
+    if (i >= total) return {-1, 0, 0, 0, 0};
+    const unsigned k = i / per, r = i - k * per;
+    const int b = (int)(r / cts);
+    const SeqSpan sp = seq_span(b, T, cu, status);
+    if ((int)k * TT < sp.len || k == 0)   // past a shorter sequence's end there is no tile
+      return {(int)k, b, (int)(r % cts), sp.len, sp.start};
+  }
+}
+
+// What a CTA's threads share beside the copied values.
+template <int NT>
+struct Shared {
+  struct {
+    float P[NT / 32][kCT], H[NT / 32][kCT];
+  } map[2];      // a warp may be a tile ahead of another's reading
+  float in[kCT];
+  Job job[4];    // a ring: the present tile, the one being copied, the one being taken
+};
+
+// Joins the threads' maps of a tile (VEC channels of S steps each) over their warps, and the warps'
+// maps in shared memory; P, H come back as the map of the warp's slots before this one.
+template <int NT, int VEC>
+__device__ __forceinline__ void join_warps(Shared<NT>& sh, int it, float (&P)[VEC], float (&H)[VEC]) {
+  constexpr int LPR = kCT / VEC;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = (threadIdx.x % LPR) * VEC;
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const float p = __shfl_up_sync(0xffffffffu, P[i], o), h = __shfl_up_sync(0xffffffffu, H[i], o);
+      if (lane >= o) {
+        H[i] = fmaf(P[i], h, H[i]);
+        P[i] *= p;
+      }
+    }
+  }
+  if (lane >= 32 - LPR) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      sh.map[it & 1].P[warp][c0 + i] = P[i];
+      sh.map[it & 1].H[warp][c0 + i] = H[i];
+    }
+  }
+  if constexpr (LPR < 32) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      P[i] = __shfl_up_sync(0xffffffffu, P[i], LPR);
+      H[i] = __shfl_up_sync(0xffffffffu, H[i], LPR);
+    }
+  }
+}
+
+// The first warp, a lane per channel: finds what enters the tile (`start` where it is the
+// sequence's first), leaves it in sh.in and returns what leaves the tile.
+template <int NT>
+__device__ __forceinline__ float look_back(Shared<NT>& sh, int it, const Job& at, float start, bool last,
+                                           int nseq, int cts, Record* rec, unsigned int* status) {
+  const int lane = threadIdx.x & 31;
+  float p = 1.f, h = 0.f, in = start;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const float pw = sh.map[it & 1].P[w][lane];
+    h = fmaf(pw, h, sh.map[it & 1].H[w][lane]);
+    p *= pw;
+  }
+  if (at.k > 0 || !last) {
+    // records of this sequence and channel, by time tile
+    const size_t step = (size_t)nseq * cts * kCT;
+    Record* r = rec + ((size_t)at.b * cts + at.ct) * kCT + lane;
+    if (at.k > 0) {
+      if (!last) publish(r + at.k * step, p, h, 0.f, kMap);
+      // the tile whose outcome is taken (the sequence's first, or the last of the group before),
+      // and the maps from there on: all asked for at once, those that were not there yet again
+      const int base = max(at.k / kGroup * kGroup - 1, 0);
+      Record before = look(r + base * step), x[kGroup - 1];
+#pragma unroll
+      for (int j = 0; j < kGroup - 1; ++j)
+        if (base + 1 + j < at.k) x[j] = look(r + (base + 1 + j) * step);
+      in = wait_for(before, r + base * step, kDone, status).out;
+#pragma unroll
+      for (int j = 0; j < kGroup - 1; ++j)
+        if (base + 1 + j < at.k) {
+          x[j] = wait_for(x[j], r + (base + 1 + j) * step, kMap, status);
+          in = fmaf(x[j].P, in, x[j].H);
+        }
+    }
+    if (!last) publish(r + at.k * step, p, h, fmaf(p, in, h), kDone);
+  }
+  sh.in[lane] = in;
+  return fmaf(p, in, h);
+}
+
+// The value that enters this thread's steps: the tile's, through the warps and slots before.
+template <int NT, int VEC>
+__device__ __forceinline__ void enter(const Shared<NT>& sh, int it, const float (&P)[VEC],
+                                      const float (&H)[VEC], float (&mine)[VEC]) {
+  constexpr int LPR = kCT / VEC;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = (threadIdx.x % LPR) * VEC;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) mine[i] = sh.in[c0 + i];
+#pragma unroll
+  for (int w = 0; w < NT / 32 - 1; ++w) {
+    if (w < warp) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) mine[i] = fmaf(sh.map[it & 1].P[w][c0 + i], mine[i], sh.map[it & 1].H[w][c0 + i]);
+    }
+  }
+  if constexpr (LPR < 32) {
+    if (lane >= LPR) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) mine[i] = fmaf(P[i], mine[i], H[i]);
+    }
+  }
+}
+
+template <typename T, int NT, int VEC, int S>
+struct FwdShared {
+  Shared<NT> sh;
+  Floats<VEC> a[S][NT];      // log_a, then the gates
+  Raw<T, VEC> x[S][NT];
+};
+
+template <typename T, int NT, int VEC, int S, int MINB>
+__global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch ws, int cts, unsigned total) {
+  constexpr int LPR = kCT / VEC, TT = NT / LPR * S;
+  extern __shared__ float4 smem[];
+  FwdShared<T, NT, VEC, S>& sm = *reinterpret_cast<FwdShared<T, NT, VEC, S>*>(smem);
+  Shared<NT>& sh = sm.sh;
+  const int tid = threadIdx.x, lane = tid & 31, slot = tid / LPR, cv = tid % LPR * VEC;
+  const T* xs = static_cast<const T*>(p.x);
+  unsigned turn = blockIdx.x;
+  auto take = [&] { return take_job<TT>(ws.next, turn, total, p.nseq, cts, p.T, p.cu_seqlens, p.status); };
+  auto copy = [&](const Job& j) {
+    const int t0 = j.k * TT + slot * S, c = j.ct * kCT + cv, n = j.k >= 0 && c < p.D ? j.len - t0 : 0;
+    const long long o = (j.start + t0) * p.D + c;
+    if (n >= S) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        cp_async<4 * VEC>(&sm.a[s][tid], p.log_a + o + s * p.D);
+        copy_x(&sm.x[s][tid], xs + o + s * p.D);
+      }
+    } else if (j.k >= 0) {   // steps past the end change nothing
+      for (int s = 0; s < S; ++s) {
+        if (s < n) {
+          cp_async<4 * VEC>(&sm.a[s][tid], p.log_a + o + s * p.D);
+          copy_x(&sm.x[s][tid], xs + o + s * p.D);
+        } else {
+          sm.a[s][tid] = Floats<VEC>{};
+          sm.x[s][tid] = Raw<T, VEC>{};
+        }
+      }
+    }
+  };
+  if (tid == 32) {
+    sh.job[0] = take();
+    sh.job[1] = sh.job[0].k >= 0 ? take() : sh.job[0];
+  }
+  __syncthreads();
+  copy(sh.job[0]);
+  for (int it = 0;; ++it) {
+    const Job at = sh.job[it & 3];
+    if (at.k < 0) break;
+    const int t0 = at.k * TT + slot * S, c = at.ct * kCT + cv, cl = at.ct * kCT + lane;
+    const bool last = (at.k + 1) * TT >= at.len;
+    const long long state = (long long)at.b * p.D + cl;
+    const float start = at.k == 0 && tid < 32 && cl < p.D && p.h0 ? p.h0[state] : 0.f;
+    const long long o = (at.start + t0) * p.D + c;
+    const unsigned odd = (unsigned)((reinterpret_cast<uintptr_t>(xs + o) >> 1) & 1);
+    float P[VEC], H[VEC], mine[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      P[i] = 1.f;
+      H[i] = 0.f;
+    }
+    cp_wait();
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      Floats<VEC> a = sm.a[s][tid];
+      const Raw<T, VEC> x = sm.x[s][tid];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        a.v[i] = gate(a.v[i]);
+        P[i] *= a.v[i];
+        H[i] = fmaf(a.v[i], H[i], x.get(i, (odd ^ (unsigned)(s * p.D)) & 1));
+      }
+      sm.a[s][tid] = a;
+    }
+    join_warps<NT, VEC>(sh, it, P, H);
+    __syncthreads();
+    if (tid == 32 && sh.job[(it + 1) & 3].k >= 0) sh.job[(it + 2) & 3] = take();
+    if (tid < 32) {
+      const float out = look_back<NT>(sh, it, at, start, last, p.nseq, cts, ws.rec, p.status);
+      if (last && p.h_last && cl < p.D) p.h_last[state] = out;
+    }
+    __syncthreads();
+    enter<NT, VEC>(sh, it, P, H, mine);
+    const int n = c < p.D ? at.len - t0 : 0;
+    float* h = p.h + o;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const Floats<VEC> a = sm.a[s][tid];
+      const Raw<T, VEC> x = sm.x[s][tid];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        mine[i] = fmaf(a.v[i], mine[i], x.get(i, (odd ^ (unsigned)(s * p.D)) & 1));
+      if (s < n) st_vec<VEC>(h + s * p.D, mine);
+    }
+    copy(sh.job[(it + 1) & 3]);
+  }
+  cp_wait();
+}
+
+template <int NT, int VEC, int S>
+struct BwdShared {
+  Shared<NT> sh;
+  Floats<VEC> a[S][NT];      // log_a, then the gates
+  Floats<VEC> dh[S][NT], h[S][NT];
+};
+
+// Backward in time, counted from the sequence's end: c_t = a_t (dh_t + c_{t+1}), c after the last
+// step being dh_last, so that g_t = dh_t + c_{t+1} and dlog_a_t = c_t h_{t-1}.
+template <int NT, int VEC, int S, int MINB>
+__global__ void __launch_bounds__(NT, MINB) glr_bwd_tiles(GlrBwdProblem p, Scratch ws, int cts, unsigned total) {
+  constexpr int LPR = kCT / VEC, TT = NT / LPR * S;
+  extern __shared__ float4 smem[];
+  BwdShared<NT, VEC, S>& sm = *reinterpret_cast<BwdShared<NT, VEC, S>*>(smem);
+  Shared<NT>& sh = sm.sh;
+  const int tid = threadIdx.x, lane = tid & 31, slot = tid / LPR, cv = tid % LPR * VEC;
+  unsigned turn = blockIdx.x;
+  auto take = [&] { return take_job<TT>(ws.next, turn, total, p.nseq, cts, p.T, p.cu_seqlens, p.status); };
+  auto copy = [&](const Job& j) {
+    const int u0 = j.k * TT + slot * S, c = j.ct * kCT + cv, n = j.k >= 0 && c < p.D ? j.len - u0 : 0;
+    const long long o = (j.start + j.len - 1 - u0) * p.D + c;
+    if (n > S) {   // the sequence's first step, which has no h before it, is not among them
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        cp_async<4 * VEC>(&sm.a[s][tid], p.log_a + o - s * p.D);
+        cp_async<4 * VEC>(&sm.dh[s][tid], p.dh + o - s * p.D);
+        cp_async<4 * VEC>(&sm.h[s][tid], p.h + o - (s + 1) * p.D);
+      }
+    } else if (j.k >= 0) {
+      for (int s = 0; s < S; ++s) {
+        if (s < n) {
+          cp_async<4 * VEC>(&sm.a[s][tid], p.log_a + o - s * p.D);
+          cp_async<4 * VEC>(&sm.dh[s][tid], p.dh + o - s * p.D);
+        } else {
+          sm.a[s][tid] = sm.dh[s][tid] = Floats<VEC>{};
+        }
+        if (s < n - 1) cp_async<4 * VEC>(&sm.h[s][tid], p.h + o - (s + 1) * p.D);
+        else if (s < n && p.h0) cp_async<4 * VEC>(&sm.h[s][tid], p.h0 + (long long)j.b * p.D + c);
+        else sm.h[s][tid] = Floats<VEC>{};
+      }
+    }
+  };
+  if (tid == 32) {
+    sh.job[0] = take();
+    sh.job[1] = sh.job[0].k >= 0 ? take() : sh.job[0];
+  }
+  __syncthreads();
+  copy(sh.job[0]);
+  for (int it = 0;; ++it) {
+    const Job at = sh.job[it & 3];
+    if (at.k < 0) break;
+    const int u0 = at.k * TT + slot * S, c = at.ct * kCT + cv, cl = at.ct * kCT + lane;
+    const bool last = (at.k + 1) * TT >= at.len;
+    const long long state = (long long)at.b * p.D + cl;
+    const float start = at.k == 0 && tid < 32 && cl < p.D && p.dh_last ? p.dh_last[state] : 0.f;
+    float P[VEC], H[VEC], mine[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      P[i] = 1.f;
+      H[i] = 0.f;
+    }
+    cp_wait();
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      Floats<VEC> a = sm.a[s][tid];
+      const Floats<VEC> d = sm.dh[s][tid];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        a.v[i] = gate(a.v[i]);
+        P[i] *= a.v[i];
+        H[i] = a.v[i] * (H[i] + d.v[i]);
+      }
+      sm.a[s][tid] = a;
+    }
+    join_warps<NT, VEC>(sh, it, P, H);
+    __syncthreads();
+    if (tid == 32 && sh.job[(it + 1) & 3].k >= 0) sh.job[(it + 2) & 3] = take();
+    if (tid < 32) {
+      const float out = look_back<NT>(sh, it, at, start, last, p.nseq, cts, ws.rec, p.status);
+      if (last && p.dh0 && cl < p.D) p.dh0[state] = out;
+    }
+    __syncthreads();
+    enter<NT, VEC>(sh, it, P, H, mine);
+    const int n = c < p.D ? at.len - u0 : 0;
+    const long long o = (at.start + at.len - 1 - u0) * p.D + c;
+    float *dx = p.dx + o, *dla = p.dlog_a + o;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const Floats<VEC> a = sm.a[s][tid], d = sm.dh[s][tid], hp = sm.h[s][tid];
+      float g[VEC], dl[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        g[i] = d.v[i] + mine[i];
+        mine[i] = a.v[i] * g[i];
+        dl[i] = mine[i] * hp.v[i];
+      }
+      if (s < n) {
+        st_vec<VEC>(dx - s * p.D, g);
+        st_vec<VEC>(dla - s * p.D, dl);
+      }
+    }
+    copy(sh.job[(it + 1) & 3]);
+  }
+  cp_wait();
+}
+
+// ---- short sequences: one thread per (sequence, channel), token by token ----
+constexpr int kWalkThreads = 128;
+
 template <typename T>
-__global__ void __launch_bounds__(kGlrThreads) glr_fwd_walk(GlrProblem p) {
-  const int c = blockIdx.x * kGlrThreads + threadIdx.x, b = blockIdx.y;
+__global__ void __launch_bounds__(kWalkThreads) glr_fwd_walk(GlrProblem p) {
+  const int c = blockIdx.x * kWalkThreads + threadIdx.x, b = blockIdx.y;
   const SeqSpan sp = seq_span(b, p.T, p.cu_seqlens, p.status);
   if (c >= p.D) return;
   const long long at = (long long)b * p.D + c;
@@ -37,14 +510,14 @@ __global__ void __launch_bounds__(kGlrThreads) glr_fwd_walk(GlrProblem p) {
 #pragma unroll 8
   for (int t = 0; t < sp.len; ++t) {
     const long long o = (long long)t * p.D;
-    h = fmaf(expf(__ldg(la + o)), h, ld_in(x + o));
+    h = fmaf(gate(__ldg(la + o)), h, ld_in(x + o));
     out[o] = h;
   }
   if (p.h_last) p.h_last[at] = h;
 }
 
-__global__ void __launch_bounds__(kGlrThreads) glr_bwd_walk(GlrBwdProblem p) {
-  const int c = blockIdx.x * kGlrThreads + threadIdx.x, b = blockIdx.y;
+__global__ void __launch_bounds__(kWalkThreads) glr_bwd_walk(GlrBwdProblem p) {
+  const int c = blockIdx.x * kWalkThreads + threadIdx.x, b = blockIdx.y;
   const SeqSpan sp = seq_span(b, p.T, p.cu_seqlens, p.status);
   if (c >= p.D) return;
   const long long at = (long long)b * p.D + c, base = sp.start * p.D + c;
@@ -55,28 +528,104 @@ __global__ void __launch_bounds__(kGlrThreads) glr_bwd_walk(GlrBwdProblem p) {
     const long long o = base + (long long)t * p.D;
     const float g = __ldg(p.dh + o) + back;
     const float past = t ? __ldg(p.h + o - p.D) : h0;
-    back = expf(__ldg(p.log_a + o)) * g;
+    back = gate(__ldg(p.log_a + o)) * g;
     p.dx[o] = g;
     p.dlog_a[o] = back * past;
   }
   if (p.dh0) p.dh0[at] = back;
 }
 
-}  // namespace
+constexpr int kWalkT = 16;   // a tile's threads have a step each at best below it
 
-cudaError_t glr_forward(const GlrProblem& p, cudaStream_t st) {
-  const dim3 grid((p.D + kGlrThreads - 1) / kGlrThreads, p.nseq);
-  count_launch();
-  if (p.in_dtype == LLATTN_BF16) glr_fwd_walk<__nv_bfloat16><<<grid, kGlrThreads, 0, st>>>(p);
-  else glr_fwd_walk<float><<<grid, kGlrThreads, 0, st>>>(p);
+constexpr int kTileSteps = 64;   // the fewest steps a tile has, which sizes the scratch
+constexpr int kSms = 148;
+
+size_t scratch_bytes(int nseq, int T, int D, int tt) {
+  return kScratchHead + (size_t)((T + tt - 1) / tt) * nseq * ((D + kCT - 1) / kCT) * kCT * sizeof(Record);
+}
+
+// The dynamic shared-memory opt-in is a per-device attribute of each kernel: asked for once.
+using Allowed = std::atomic<bool>[64];
+
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, Allowed& allowed, size_t smem) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (allowed[dev].load()) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) allowed[dev].store(true);
+  return e;
+}
+
+template <typename Problem>
+cudaError_t launch_tiles(void (*kernel)(Problem, Scratch, int, unsigned), Allowed& allowed,
+                         const Problem& p, int tt, int threads, int ctas_per_sm, size_t smem,
+                         void* ws, cudaStream_t st) {
+  const int cts = (p.D + kCT - 1) / kCT, tiles = (p.T + tt - 1) / tt;
+  Scratch s{static_cast<unsigned*>(ws),
+            reinterpret_cast<Record*>(static_cast<char*>(ws) + kScratchHead)};
+  const unsigned total = (unsigned)tiles * p.nseq * cts, most = kSms * ctas_per_sm;
+  cudaError_t e = allow_smem(kernel, allowed, smem);
+  if (e != cudaSuccess) return e;
+  if (tiles == 1) s = {nullptr, nullptr};
+  else if ((e = cudaMemsetAsync(ws, 0, scratch_bytes(p.nseq, p.T, p.D, tt), st)) != cudaSuccess) return e;
+  kernel<<<total < most ? total : most, threads, smem, st>>>(p, s, cts, total);
   return cudaGetLastError();
 }
 
-cudaError_t glr_backward(const GlrBwdProblem& p, cudaStream_t st) {
-  const dim3 grid((p.D + kGlrThreads - 1) / kGlrThreads, p.nseq);
+template <typename T, int NT, int VEC, int S, int MINB>
+cudaError_t fwd_tiles(const GlrProblem& p, void* ws, cudaStream_t st) {
+  static Allowed allowed;
+  return launch_tiles(glr_fwd_tiles<T, NT, VEC, S, MINB>, allowed, p, NT * VEC / kCT * S, NT, MINB,
+                      sizeof(FwdShared<T, NT, VEC, S>), ws, st);
+}
+template <int NT, int VEC, int S, int MINB>
+cudaError_t bwd_tiles(const GlrBwdProblem& p, void* ws, cudaStream_t st) {
+  static Allowed allowed;
+  return launch_tiles(glr_bwd_tiles<NT, VEC, S, MINB>, allowed, p, NT * VEC / kCT * S, NT, MINB,
+                      sizeof(BwdShared<NT, VEC, S>), ws, st);
+}
+
+bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+template <typename T>
+cudaError_t fwd(const GlrProblem& p, void* ws, cudaStream_t st) {
+  if (p.T <= kWalkT) {
+    const dim3 grid((p.D + kWalkThreads - 1) / kWalkThreads, p.nseq);
+    glr_fwd_walk<T><<<grid, kWalkThreads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  const bool vec = p.D % 4 == 0 && aligned_to(p.x, 4 * sizeof(T)) && aligned_to(p.log_a, 16) &&
+                   aligned_to(p.h, 16);
+  if (!vec) return fwd_tiles<T, 128, 1, 32, 4>(p, ws, st);
+  return fwd_tiles<T, 256, 4, 8, 3>(p, ws, st);
+}
+
+}  // namespace
+
+size_t glr_workspace_bytes(int nseq, int T, int D) {
+  return T <= kTileSteps ? 0 : scratch_bytes(nseq, T, D, kTileSteps);
+}
+
+cudaError_t glr_forward(const GlrProblem& p, void* ws, cudaStream_t st) {
   count_launch();
-  glr_bwd_walk<<<grid, kGlrThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return p.in_dtype == LLATTN_BF16 ? fwd<__nv_bfloat16>(p, ws, st) : fwd<float>(p, ws, st);
+}
+
+cudaError_t glr_backward(const GlrBwdProblem& p, void* ws, cudaStream_t st) {
+  count_launch();
+  if (p.T <= kWalkT) {
+    const dim3 grid((p.D + kWalkThreads - 1) / kWalkThreads, p.nseq);
+    glr_bwd_walk<<<grid, kWalkThreads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  const void* ptrs[6] = {p.log_a, p.h, p.h0, p.dh, p.dx, p.dlog_a};
+  bool vec = p.D % 4 == 0;
+  for (const void* q : ptrs) vec = vec && aligned_to(q, 16);
+  if (!vec) return bwd_tiles<128, 1, 16, 6>(p, ws, st);
+  return bwd_tiles<256, 4, 4, 4>(p, ws, st);
 }
 
 }  // namespace llattn

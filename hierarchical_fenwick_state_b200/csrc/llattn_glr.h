@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <cstddef>
 
 namespace llattn {
 
@@ -31,7 +32,10 @@ struct GlrBwdProblem {
   unsigned int* status;
 };
 
-cudaError_t glr_forward(const GlrProblem& p, cudaStream_t st);
-cudaError_t glr_backward(const GlrBwdProblem& p, cudaStream_t st);
+// Scratch of either call (0 where a sequence fits one tile).
+size_t glr_workspace_bytes(int nseq, int T, int D);
+
+cudaError_t glr_forward(const GlrProblem& p, void* ws, cudaStream_t st);
+cudaError_t glr_backward(const GlrBwdProblem& p, void* ws, cudaStream_t st);
 
 }  // namespace llattn

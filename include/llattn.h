@@ -517,13 +517,19 @@ LLATTN_API llattn_status llattn_qk_norm_rope_bwd(
  *   h_last     fp32 [B, D] or NULL: the state after the last token (h0 or 0 for an empty
  *              sequence).  May be h0 itself: a decoding step is T = 1 with one state buffer.
  *   cu_seqlens as in llattn_fwd.  B, D <= 65535, 0 <= T <= 2^24.
- * Pointers aligned to their type (16-byte alignment and D a multiple of 8 run fastest); no
- * output may overlap an input or another output, h_last == h0 excepted.  No scratch memory.
- * Asynchronous on `stream`.
+ *   workspace  caller-owned device scratch of llattn_glr_workspace_bytes() bytes (256-byte
+ *              aligned; its contents do not matter), or NULL for the library's per-device buffer
+ *              (as llattn_fwd: calls that overlap need workspaces of their own).  A query of 0
+ *              bytes needs none.
+ * Pointers aligned to their type (16-byte alignment and D a multiple of 4 run fastest); no
+ * output may overlap an input or another output, h_last == h0 excepted.  The same call gives the
+ * same bits.  Asynchronous on `stream`.
  */
+LLATTN_API llattn_status llattn_glr_workspace_bytes(int B, int T, int D, size_t* bytes);
 LLATTN_API llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float* log_a,
                                         const float* h0, float* h, float* h_last, int B, int T,
-                                        int D, const int* cu_seqlens, void* stream);
+                                        int D, const int* cu_seqlens, void* workspace,
+                                        size_t workspace_bytes, void* stream);
 
 /*
  * llattn_glr_bwd - its gradients from dh (at h) and dh_last (at h_last), with h as llattn_glr_fwd
@@ -538,7 +544,8 @@ LLATTN_API llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float
 LLATTN_API llattn_status llattn_glr_bwd(const float* log_a, const float* h, const float* h0,
                                         const float* dh, const float* dh_last, float* dx,
                                         float* dlog_a, float* dh0, int B, int T, int D,
-                                        const int* cu_seqlens, void* stream);
+                                        const int* cu_seqlens, void* workspace,
+                                        size_t workspace_bytes, void* stream);
 
 /*
  * The decoding state in 8 bits: a quarter of llattn_decode_step's state and of the bytes that a

@@ -1,10 +1,14 @@
 """The gated linear recurrence on the GPU, forward and backward, against the recurrence in 64 bits.
 
-Bounds (u = 2^-24).  Each step multiplies by exp(log_a), off by at most 2 steps (4 u), and rounds
-the product and the sum; where a walk is split, the parts' gates are products (one more rounding of
+Bounds (u = 2^-24).  Each step multiplies by exp(log_a), off by at most 2 steps (4 u) and, as
+2^(log_a log2 e), by the roundings of the exponent's product and of log2 e: an error d of the exponent
+x log2 e is one of d ln 2 relative, and |d| <= |x| log2 e (u + 0.23 u), so 1.25 |x| u.  It rounds the
+product and the sum; where a walk is split, the parts' gates are products (one more rounding of
 u per step) and joining them adds a rounding or two per part.  So with M_t = a_t M_{t-1} + |x_t|
-(M_{-1} = |h0|), an error grows as E_t = a_t E_{t-1} + 16 u M_t, whatever the split.  The backward
-recurrence is the same with the gates one step on; dlog_a = g a h_{t-1} adds 8 u of itself.
+(M_{-1} = |h0|), an error grows as E_t = a_t E_{t-1} + 16 u M_t, whatever the split (the exponent's part
+is 1.25 |x| e^x u M_{t-1} <= 0.46 u M_{t-1}, and no part for a gate above 1: those are below e^0.1).
+The backward recurrence is the same with the gates one step on; dlog_a = g a h_{t-1} adds 8 u and the
+exponent's 1.25 |log_a| u of itself.
 
 Those are relative errors, which hold for results of at least 2^-126, fp32's smallest normal number.
 Below it a result is off by up to half of 2^-149, or by all of itself where it is flushed to zero,
@@ -95,9 +99,10 @@ class Case:
                 err = err + 16 * U * m
                 past = a[t] * (h[t - 1] if t > s else h0)
                 dx[t], dla[t], E[t] = g, g * past, err
-                Ela[t] = (err + 8 * U * g.abs()) * past.abs()
+                off = 8 * U + torch.where(a[t] > 0, 1.25 * U * self.la[t].double().abs(), 0.0)
+                Ela[t] = (err + off * g.abs()) * past.abs()
                 c, m, err = a[t] * g, a[t] * m, a[t] * err
-            d0[b], e0[b] = c, err + 8 * U * c.abs()
+            d0[b], e0[b] = c, err + 8 * U * m   # a_0 g_0: its exponent's part as in E
         return dx, dla, d0, E, Ela, e0
 
 

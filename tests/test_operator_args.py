@@ -75,8 +75,8 @@ def test_qk_empty_calls_and_workspace():
 
 
 GLR = dict(in_dtype=BF16, x=1 * M, log_a=2 * M, h0=None, h=3 * M, h_last=None, B=2, T=16, D=64,
-           cu=None, stream=None)
-GLR_ORDER = "in_dtype x log_a h0 h h_last B T D cu stream"
+           cu=None, ws=None, wsn=0, stream=None)
+GLR_ORDER = "in_dtype x log_a h0 h h_last B T D cu ws wsn stream"
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -95,8 +95,8 @@ def test_glr_refusals(kw, status):
 
 
 GLRB = dict(log_a=1 * M, h=2 * M, h0=None, dh=3 * M, dh_last=None, dx=4 * M, dlog_a=5 * M, dh0=None,
-            B=2, T=16, D=64, cu=None, stream=None)
-GLRB_ORDER = "log_a h h0 dh dh_last dx dlog_a dh0 B T D cu stream"
+            B=2, T=16, D=64, cu=None, ws=None, wsn=0, stream=None)
+GLRB_ORDER = "log_a h h0 dh dh_last dx dlog_a dh0 B T D cu ws wsn stream"
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -107,6 +107,16 @@ GLRB_ORDER = "log_a h h0 dh dh_last dx dlog_a dh0 B T D cu stream"
 ])
 def test_glr_backward_refusals(kw, status):
     assert _call("llattn_glr_bwd", GLRB_ORDER, GLRB, kw) == status
+
+
+def test_glr_workspace():
+    assert binding.glr_workspace_bytes(64, 1, 2048) == 0
+    assert binding.glr_workspace_bytes(0, 5000, 64) == 0
+    n = binding.glr_workspace_bytes(1, 65536, 2048)
+    assert 0 < n < 65536 * 2048      # small beside the 10 bytes per element of a call
+    for bad in ((-1, 1, 1), (1, 1 << 25, 1), (1, 1, 65536), (65535, 1 << 24, 64)):
+        with pytest.raises(binding.LLAttnError):
+            binding.glr_workspace_bytes(*bad)
 
 
 def test_glr_empty_calls():
