@@ -29,7 +29,8 @@ EXPORTS = (
     "llattn_segment_plan", "llattn_set_segment_chunks", "llattn_gdn_fwd",
     "llattn_prefill_state", "llattn_qk_norm_rope", "llattn_qk_norm_rope_bwd_workspace_bytes",
     "llattn_qk_norm_rope_bwd", "llattn_glr_workspace_bytes", "llattn_glr_fwd", "llattn_glr_bwd",
-    "llattn_decode_q8_state_bytes", "llattn_decode_step_q8", "llattn_prefill_state_q8",
+    "llattn_decode_q8_state_bytes", "llattn_decode_step_q8",
+    "llattn_prefill_q8_workspace_bytes", "llattn_prefill_state_q8",
     "llattn_read_state_q8",
 )
 
@@ -118,8 +119,10 @@ def lib():
     L.llattn_decode_q8_state_bytes.argtypes = [i, i, i, i, i, szp]
     L.llattn_decode_step_q8.restype = i
     L.llattn_decode_step_q8.argtypes = [i, vp, vp, vp, f_p, f_p, i_p, vp, f_p, i, i, i, i, i, vp]
+    L.llattn_prefill_q8_workspace_bytes.restype = i
+    L.llattn_prefill_q8_workspace_bytes.argtypes = [i, i, i, i, i, i, szp]
     L.llattn_prefill_state_q8.restype = i
-    L.llattn_prefill_state_q8.argtypes = [i, vp, vp, f_p, vp, i, i, i, i, i, i, i_p, vp]
+    L.llattn_prefill_state_q8.argtypes = [i, vp, vp, f_p, vp, i, i, i, i, i, i, i_p, vp, sz, vp]
     L.llattn_read_state_q8.restype = i
     L.llattn_read_state_q8.argtypes = [vp, i_p, vp, i, i, i, i, i, i, vp]
     L.llattn_profile.restype = i
@@ -622,18 +625,17 @@ def glr_workspace_bytes(B: int, T: int, D: int) -> int:
     return int(n.value)
 
 
-def _glr_workspace(workspace, B, T, D, dev, stream):
-    """The call's scratch: the caller's, or torch's for this call alone (none where none is needed)."""
+def _workspace(workspace, need, dev, stream):
+    """A call's scratch: the caller's, or torch's for this call alone (none where none is needed)."""
     import torch
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
-    n = glr_workspace_bytes(B, T, D)
-    if n == 0:
+    if need == 0:
         return None, 0
     if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=dev), n
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
     with torch.cuda.stream(stream):   # torch hands it on in that stream's order
-        return torch.empty(n, dtype=torch.uint8, device=dev), n
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
 
 
 def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[int] = None,
@@ -657,7 +659,7 @@ def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[
         out = torch.empty(x.shape, dtype=f32, device=dev)
     else:
         _expect(out, "out", f32, x.shape, dev)
-    ws, ws_n = _glr_workspace(workspace, B, T, D, dev, stream)
+    ws, ws_n = _workspace(workspace, glr_workspace_bytes(B, T, D), dev, stream)
     _on_device(lib().llattn_glr_fwd, dev, stream, "llattn_glr_fwd",
                (dt, _ptr(x), _ptr(log_a), _ptr(h0), _ptr(out), _ptr(h_last), B, T, D,
                 _ptr(cu_seqlens), _ptr(ws), ws_n))
@@ -693,7 +695,7 @@ def glr_backward(log_a, h, dh, *, h0=None, dh_last=None, cu_seqlens=None, T: Opt
         _expect(t, "grads['h0']", f32, None, dev)
         if t is not None and t.numel() != B * D:
             raise ValueError(f"grads['h0'] must have shape {state}")
-    ws, ws_n = _glr_workspace(workspace, B, T, D, dev, stream)
+    ws, ws_n = _workspace(workspace, glr_workspace_bytes(B, T, D), dev, stream)
     _on_device(lib().llattn_glr_bwd, dev, stream, "llattn_glr_bwd",
                (_ptr(log_a), _ptr(h), _ptr(h0), _ptr(dh), _ptr(dh_last), _ptr(grads["x"]),
                 _ptr(grads["log_a"]), _ptr(grads.get("h0")), B, T, D, _ptr(cu_seqlens), _ptr(ws),
@@ -737,7 +739,17 @@ def decode_step_q8(q, k, v, log_a, lam, pos, state, out, B, H, L, dk, dv, stream
     return out
 
 
-def prefill_state_q8(k, v, log_a, state, B, H, T, L, dk, dv, cu_seqlens=None, stream=None):
+def prefill_q8_workspace_bytes(B: int, H: int, T: int, L: int, dk: int, dv: int) -> int:
+    """Bytes of scratch of prefill_state_q8 (llattn_prefill_q8_workspace_bytes)."""
+    n = ctypes.c_size_t(0)
+    _check(lib().llattn_prefill_q8_workspace_bytes(int(B), int(H), int(T), int(L), int(dk), int(dv),
+                                                   ctypes.byref(n)),
+           "llattn_prefill_q8_workspace_bytes")
+    return int(n.value)
+
+
+def prefill_state_q8(k, v, log_a, state, B, H, T, L, dk, dv, cu_seqlens=None, workspace=None,
+                     stream=None):
     """llattn_prefill_state_q8: prefill_state into the 8-bit state.  k, v dense [B,T,H,d] or packed
     [total,H,d] (bf16 or fp32), log_a fp32 [..,H], cu_seqlens int32 [B+1] or None."""
     import torch
@@ -747,9 +759,10 @@ def prefill_state_q8(k, v, log_a, state, B, H, T, L, dk, dv, cu_seqlens=None, st
     _expect(v, "v", k.dtype, lead + (H, dv), dev)
     _expect(log_a, "log_a", torch.float32, lead + (H,), dev)
     _expect(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    ws, ws_n = _workspace(workspace, prefill_q8_workspace_bytes(B, H, T, L, dk, dv), dev, stream)
     _on_device(lib().llattn_prefill_state_q8, dev, stream, "llattn_prefill_state_q8",
                (dt, _ptr(k), _ptr(v), _ptr(log_a), _ptr(state), B, H, T, L, dk, dv,
-                _ptr(cu_seqlens)))
+                _ptr(cu_seqlens), _ptr(ws), ws_n))
     return state
 
 

@@ -983,9 +983,21 @@ llattn_status llattn_decode_step_q8(int in_dtype, const void* q, const void* k, 
   return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
 }
 
+llattn_status llattn_prefill_q8_workspace_bytes(int B, int H, int T, int L, int dk, int dv,
+                                                size_t* bytes) {
+  if (!bytes) return LLATTN_ERR_ARG;
+  size_t state_bytes = 0;
+  const llattn_status s = llattn_decode_q8_state_bytes(B, H, L, dk, dv, &state_bytes);
+  if (s != LLATTN_OK) return s;
+  if (T < 0 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
+  *bytes = B == 0 || H == 0 ? 0 : llattn::q8_prefill_workspace_bytes(B, H, T, L, dk, dv);
+  return LLATTN_OK;
+}
+
 llattn_status llattn_prefill_state_q8(int in_dtype, const void* k, const void* v,
                                       const float* log_a, void* state, int B, int H, int T, int L,
-                                      int dk, int dv, const int* cu_seqlens, void* stream) {
+                                      int dk, int dv, const int* cu_seqlens, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
   if (in_dtype != LLATTN_F32 && in_dtype != LLATTN_BF16) return LLATTN_ERR_DTYPE;
   size_t state_bytes = 0;
   llattn_status s = llattn_decode_q8_state_bytes(B, H, L, dk, dv, &state_bytes);
@@ -1006,9 +1018,14 @@ llattn_status llattn_prefill_state_q8(int in_dtype, const void* k, const void* v
   DeviceState* ds = nullptr;
   int dev = 0;
   if ((s = device_state(&ds, &dev)) != LLATTN_OK) return s;
+  void* ws = nullptr;
+  std::unique_lock<std::mutex> lock(g_mu, std::defer_lock);
+  if ((s = pick_workspace(ds, llattn::q8_prefill_workspace_bytes(B, H, T, L, dk, dv), workspace,
+                          workspace_bytes, lock, &ws)) != LLATTN_OK)
+    return s;
   llattn::Q8PrefillProblem p{in_dtype, k, v, log_a, llattn::q8_state_views(state, B, H, L, dk, dv),
                              B, H, T, L, dk, dv, cu_seqlens, ds->status};
-  const cudaError_t err = llattn::q8_prefill(p, static_cast<cudaStream_t>(stream));
+  const cudaError_t err = llattn::q8_prefill(p, ws, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
 }
 

@@ -65,7 +65,8 @@ struct Q8ReadProblem {
 };
 
 cudaError_t q8_step(const Q8StepProblem& p, cudaStream_t st);
-cudaError_t q8_prefill(const Q8PrefillProblem& p, cudaStream_t st);
+size_t q8_prefill_workspace_bytes(int B, int H, int T, int L, int dk, int dv);
+cudaError_t q8_prefill(const Q8PrefillProblem& p, void* ws, cudaStream_t st);
 cudaError_t q8_read(const Q8ReadProblem& p, cudaStream_t st);
 
 }  // namespace llattn

@@ -26,7 +26,7 @@ struct QkProblem {
 };
 
 // Rows of weight-gradient partials the backward's scratch holds (one per CTA at most).
-constexpr int kQkMaxCtas = 148 * 4;
+constexpr int kQkMaxCtas = 148 * 2;
 inline size_t qk_bwd_workspace_bytes(int d, bool weights) {
   return weights ? (size_t)kQkMaxCtas * 2 * d * sizeof(float) : 0;
 }

@@ -562,8 +562,12 @@ LLATTN_API llattn_status llattn_glr_bwd(const float* log_a, const float* h, cons
  *   has in llattn_decode_step, then exps uint8 [B, H, L-1, dk, dv/32]: e + 127, 0 for a block of
  *   zeros, 255 for one that was to hold an infinity or NaN (it reads as NaN).
  * llattn_decode_step_q8 - llattn_decode_step on such a state; arguments as there.
- * llattn_prefill_state_q8 - llattn_prefill_state on such a state; arguments as there.  The sums
- *   over a bucket are accumulated in fp32.
+ * llattn_prefill_state_q8 - llattn_prefill_state on such a state; arguments as there, and scratch:
+ *   workspace, caller-owned device memory of llattn_prefill_q8_workspace_bytes() bytes (256-byte
+ *   aligned; 64 MB of sums at most where T <= 2^24 / (B*H), its contents do not matter), or NULL
+ *   for the library's per-device buffer (as llattn_fwd: calls that overlap need their own).  The
+ *   sums over a bucket run on the tensor cores with fp32 accumulation, every operand that is not a
+ *   bf16 split into two; the same call gives the same bits.
  * llattn_read_state_q8 - the held values, as slots store them (their pending gates not applied),
  *   exactly for both types: slot NULL gives every slot, out [B, H, L-1, dk, dv] (slots that hold
  *   no level read as whatever they last held); a DEVICE int32 array slot [B] gives slot slot[b]
@@ -578,10 +582,13 @@ LLATTN_API llattn_status llattn_decode_step_q8(int in_dtype, const void* q, cons
                                                const float* lam, const int* pos, void* state,
                                                float* out, int B, int H, int L, int dk, int dv,
                                                void* stream);
+LLATTN_API llattn_status llattn_prefill_q8_workspace_bytes(int B, int H, int T, int L, int dk,
+                                                           int dv, size_t* bytes);
 LLATTN_API llattn_status llattn_prefill_state_q8(int in_dtype, const void* k, const void* v,
                                                  const float* log_a, void* state, int B, int H,
                                                  int T, int L, int dk, int dv,
-                                                 const int* cu_seqlens, void* stream);
+                                                 const int* cu_seqlens, void* workspace,
+                                                 size_t workspace_bytes, void* stream);
 LLATTN_API llattn_status llattn_read_state_q8(const void* state, const int* slot, void* out,
                                               int out_dtype, int B, int H, int L, int dk, int dv,
                                               void* stream);

@@ -141,8 +141,8 @@ def test_step_q8_refusals(kw, status):
 
 
 PRE = dict(in_dtype=BF16, k=1 * M, v=2 * M, log_a=3 * M, state=64 * M, B=2, H=3, T=100, L=14, dk=64, dv=64,
-           cu=None, stream=None)
-PRE_ORDER = "in_dtype k v log_a state B H T L dk dv cu stream"
+           cu=None, ws=None, wsn=0, stream=None)
+PRE_ORDER = "in_dtype k v log_a state B H T L dk dv cu ws wsn stream"
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -166,6 +166,16 @@ READ_ORDER = "state slot out out_dtype B H L dk dv stream"
 ])
 def test_read_q8_refusals(kw, status):
     assert _call("llattn_read_state_q8", READ_ORDER, READ, kw) == status
+
+
+def test_prefill_q8_workspace():
+    assert binding.prefill_q8_workspace_bytes(0, 4, 100, 14, 64, 64) == 0
+    assert binding.prefill_q8_workspace_bytes(2, 4, 100, 1, 64, 64) == 0
+    for B, H, T, dk, dv in ((8, 16, 16384, 64, 64), (32, 32, 8192, 64, 64), (1, 1, 1 << 24, 128, 128)):
+        assert 0 < binding.prefill_q8_workspace_bytes(B, H, T, 25, dk, dv) <= (64 << 20) + (1 << 18)
+    for bad in ((-1, 1, 1, 14, 64, 64), (1, 1, 1 << 25, 14, 64, 64), (1, 1, 1, 33, 64, 64), (1, 1, 1, 14, 48, 64)):
+        with pytest.raises(binding.LLAttnError):
+            binding.prefill_q8_workspace_bytes(*bad)
 
 
 def test_q8_empty_calls_and_state_bytes():
