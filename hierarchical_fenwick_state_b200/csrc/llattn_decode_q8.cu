@@ -25,6 +25,7 @@
 #include "llattn_common.cuh"
 #include "llattn_decode_q8.h"
 #include "llattn_internal.h"
+#include "llattn_tc_ptx.cuh"
 
 namespace llattn {
 namespace {
@@ -60,13 +61,67 @@ __device__ __forceinline__ void unpack16(const uint4& u, float (&x)[16]) {
   for (int i = 0; i < 16; ++i) x[i] = (float)(int)(signed char)(w[i >> 2] >> (8 * (i & 3)));
 }
 
+// Pairs of fp32 in one register pair: one instruction for two sums or products.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Sixteen codes as eight pairs, exactly: a code plus 128 in the last byte of 2^23's bits is
+// 2^23 + 128 + code, one byte permutation each, and the pairs' offset comes off in one sum (a
+// conversion instruction per code would take four times the issue slots).
+__device__ __forceinline__ void pairs16(const uint4& u, uint64_t (&x)[8]) {
+  const unsigned w[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
+  const uint64_t off = pair(-8388736.f, -8388736.f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int s = 2 * (i & 1);
+    x[i] = add2(pair(__uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440 + s)),
+                     __uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7441 + s))), off);
+  }
+}
+
+// Sixteen values, a block's half beside its other half on the neighbouring lane, as codes; returns
+// the block's exponent code.
+__device__ __forceinline__ unsigned store_codes(const uint64_t (&v)[8], int8_t* to) {
+  float x[16];
+  unsigned top = 0u, w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int c = 0; c < 8; ++c) unpair(v[c], x[2 * c], x[2 * c + 1]);
+#pragma unroll
+  for (int c = 0; c < 16; ++c) top = max(top, __float_as_uint(x[c]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const unsigned e = q8_exp(top);
+  const float inv = q8_inverse(e);
+#pragma unroll
+  for (int c = 0; c < 16; ++c) w[c >> 2] |= (unsigned)(q8_code(x[c], inv, e) & 0xff) << (8 * (c & 3));
+  *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+  return e;
+}
+
 // The step's CTA takes one 32-column block of one (head, sequence): thread (r, half) owns 16
-// columns of row r in every level.
+// columns of row r in every level.  Levels come lowest first, kStepBatch of them asked for at a
+// time, and those that the carry takes (slots 0..m-1) are the first m.
+constexpr int kStepBatch = 8;
+
 template <typename Tin, int DK>
-__global__ void __launch_bounds__(2 * DK) q8_step_kernel(Q8StepProblem p) {
+__global__ void __launch_bounds__(2 * DK, 640 / (2 * DK)) q8_step_kernel(Q8StepProblem p) {
   constexpr int kWarps = 2 * DK / 32;
   __shared__ float s_lam[32], s_w[32];
-  __shared__ int s_slot[32];
   __shared__ float s_red[kWarps][32];
   __shared__ float s_qk[kWarps];
 
@@ -78,79 +133,91 @@ __global__ void __launch_bounds__(2 * DK) q8_step_kernel(Q8StepProblem p) {
     if (tid == 0) atomicOr(p.status, LLATTN_DEV_DECODE_POS);
     return;
   }
-  const unsigned un = (unsigned)n;
-  const int m = __ffs(~un) - 1, cnt = __popc(un);
-  const unsigned par = un & 1u, par1 = par ^ 1u;
+  const unsigned un = (unsigned)n, par = un & 1u;
+  const int m = __ffs(~un) - 1;
   const size_t bh = (size_t)b * p.H + h;
+  const int r = tid >> 1, half = tid & 1, col = cb * 32 + half * kStepVals;
+  const size_t slot_codes = (size_t)DK * p.dv, slot_exps = (size_t)DK * nb;
+  int8_t* codes = p.s.codes + bh * nslot * slot_codes + (size_t)r * p.dv + col;
+  uint8_t* exps = p.s.exps + bh * nslot * slot_exps + (size_t)r * nb + cb;
+
+  uint4 raw[kStepBatch];
+  unsigned ex[kStepBatch];
+  auto fetch = [&](unsigned u) {
+#pragma unroll
+    for (int i = 0; i < kStepBatch; ++i) {
+      if (u == 0u) break;
+      const int j = __ffs(u) - 1;
+      raw[i] = __ldcs(reinterpret_cast<const uint4*>(codes + j * slot_codes));
+      ex[i] = exps[j * slot_exps];
+      u &= u - 1u;
+    }
+  };
+  fetch(un);
+
   const float la = __ldg(p.log_a + bh);
   float* gate = p.s.gate + bh * 2 * nslot;
-
   if (tid < p.L) s_lam[tid] = __ldg(p.lam + bh * p.L + tid);
-  if (tid < nslot && ((un >> tid) & 1u)) {
-    const int rank = __popc(un & ((1u << tid) - 1u));
-    s_slot[rank] = tid;
-    s_w[rank] = expf(gate[par * nslot + tid] + la);
-  }
-  const int r = tid >> 1, half = tid & 1;
+  if (tid < nslot && ((un >> tid) & 1u)) s_w[tid] = expf(gate[par * nslot + tid] + la);
   const float qr = ld_in(static_cast<const Tin*>(p.q) + bh * DK + r);
   const float kr = ld_in(static_cast<const Tin*>(p.k) + bh * DK + r);
+  const Tin* v = static_cast<const Tin*>(p.v) + bh * p.dv + col;
+  uint64_t carry[8], part[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    carry[i] = pair(kr * ld_in(v + 2 * i), kr * ld_in(v + 2 * i + 1));
+    part[i] = 0ull;
+  }
   float qk = half ? 0.f : qr * kr;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, o);
   if (lane == 0) s_qk[warp] = qk;
   __syncthreads();
 
-  const int col = cb * 32 + half * kStepVals;
-  const Tin* v = static_cast<const Tin*>(p.v) + bh * p.dv + col;
-  float carry[kStepVals], part[kStepVals];
+  for (unsigned u = un; u != 0u;) {
+    unsigned rest = u;
 #pragma unroll
-  for (int i = 0; i < kStepVals; ++i) {
-    carry[i] = kr * ld_in(v + i);
-    part[i] = 0.f;
-  }
-  const size_t slot_codes = (size_t)DK * p.dv, slot_exps = (size_t)DK * nb;
-  int8_t* codes = p.s.codes + bh * nslot * slot_codes + (size_t)r * p.dv + col;
-  uint8_t* exps = p.s.exps + bh * nslot * slot_exps + (size_t)r * nb + cb;
-#pragma unroll 4
-  for (int i = 0; i < cnt; ++i) {
-    const int j = s_slot[i];
-    const float w = s_w[i];
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(codes + j * slot_codes));
-    const float sc = q8_scale(exps[j * slot_exps]);
-    float x[kStepVals];
-    unpack16(u, x);
-    const float f = qr * sc * (w * s_lam[j + 1]);
+    for (int i = 0; i < kStepBatch; ++i) {
+      if (rest == 0u) break;
+      const int j = __ffs(rest) - 1;
+      rest &= rest - 1u;
+      const float g = q8_scale(ex[i]) * s_w[j], f = qr * g * s_lam[j + 1];
+      const uint64_t f2 = pair(f, f);
+      uint64_t x[8];
+      pairs16(raw[i], x);
 #pragma unroll
-    for (int c = 0; c < kStepVals; ++c) part[c] = fmaf(f, x[c], part[c]);
-    if (j < m) {
-      const float g = sc * w;
+      for (int c = 0; c < 8; ++c) part[c] = fma2(f2, x[c], part[c]);
+      if (j < m) {
+        const uint64_t g2 = pair(g, g);
 #pragma unroll
-      for (int c = 0; c < kStepVals; ++c) carry[c] = fmaf(g, x[c], carry[c]);
+        for (int c = 0; c < 8; ++c) carry[c] = fma2(g2, x[c], carry[c]);
+      }
     }
+    u = rest;
+    fetch(u);
   }
 
   if (m < nslot) {   // the carried level, rounded to its block's power of two
-    unsigned top = 0u;
-#pragma unroll
-    for (int c = 0; c < kStepVals; ++c) top = max(top, __float_as_uint(carry[c]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    const unsigned e = q8_exp(top);
-    const float inv = q8_inverse(e);
-    unsigned w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int c = 0; c < kStepVals; ++c)
-      w[c >> 2] |= (unsigned)(q8_code(carry[c], inv, e) & 0xff) << (8 * (c & 3));
-    *reinterpret_cast<uint4*>(codes + m * slot_codes) = make_uint4(w[0], w[1], w[2], w[3]);
+    const unsigned e = store_codes(carry, codes + m * slot_codes);
     if (half == 0) exps[m * slot_exps] = (uint8_t)e;
   }
 
-  // readout: sum over the rows (lanes of one parity, then warps)
+  // readout: the 16 columns' sums over the warp's 16 rows, halving the columns a lane carries at
+  // every exchange; a lane ends with one column
+  float x[kStepVals];
 #pragma unroll
-  for (int c = 0; c < kStepVals; ++c) {
+  for (int c = 0; c < 8; ++c) unpair(part[c], x[2 * c], x[2 * c + 1]);
 #pragma unroll
-    for (int o = 2; o < 32; o <<= 1) part[c] += __shfl_xor_sync(0xffffffffu, part[c], o);
-    if (lane < 2) s_red[warp][lane * kStepVals + c] = part[c];
+  for (int o = 16, k = 8; o > 1; o >>= 1, k >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= k) break;
+      const float keep = up ? x[i + k] : x[i], send = up ? x[i] : x[i + k];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
   }
+  s_red[warp][half * kStepVals + (lane >> 1)] = x[0];   // (bit by bit, lane / 2 is the column)
   __syncthreads();
   if (tid < 32) {
     float s = 0.f, qkt = 0.f;
@@ -163,11 +230,223 @@ __global__ void __launch_bounds__(2 * DK) q8_step_kernel(Q8StepProblem p) {
     p.out[bh * p.dv + c] = fmaf(s_lam[0] * qkt, ld_in(static_cast<const Tin*>(p.v) + bh * p.dv + c), s);
   }
   if (cb == 0 && tid < nslot && (((un + 1u) >> tid) & 1u))
-    gate[par1 * nslot + tid] = (tid == m) ? 0.f : gate[par * nslot + tid] + la;
+    gate[(par ^ 1u) * nslot + tid] = (tid == m) ? 0.f : gate[par * nslot + tid] + la;
 }
+
+// ---- the step of a large batch ----
+//
+// One CTA per (head, sequence) there: a whole slot is one run of dk * dv bytes, so a producer warp
+// copies the occupied slots, lowest first, into a ring in shared memory (a bulk copy each, the
+// block exponents beside it), and the other warps read them out.  Bytes in flight wait in shared
+// memory in place of registers, which lets six CTAs of 64 x 64 states share an SM.
+template <int DK, int DV>
+struct Ring {
+  static constexpr int kSlot = DK * DV, kExps = DK * (DV / 32);
+  static constexpr int kStages = kSlot <= 2048 ? 16 : kSlot <= 8192 ? 8 : 6;
+  static constexpr int kChunks = kSlot / 16;
+  static constexpr int kThreads = kChunks <= 64 ? 64 : kChunks / 2 < 64 ? 64 : kChunks / 2;   // readers
+  static constexpr int kRows = kChunks / kThreads;         // rows of a reader, 16 columns of each
+  static constexpr int kBytes = kStages * (kSlot + kExps);
+};
+
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// The thread's copies so far arrive at the barrier when they are done.
+__device__ __forceinline__ void arrive_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
+
+template <typename Tin, int DK, int DV>
+__global__ void __launch_bounds__(Ring<DK, DV>::kThreads + 32) q8_step_ring_kernel(Q8StepProblem p) {
+  using R = Ring<DK, DV>;
+  constexpr int NT = R::kThreads, kWarps = NT / 32, CPR = DV / 16, NB = DV / 32, NS = R::kStages;
+  extern __shared__ float4 ring_smem[];
+  int8_t* s_codes = reinterpret_cast<int8_t*>(ring_smem);
+  uint8_t* s_exps = reinterpret_cast<uint8_t*>(s_codes + NS * R::kSlot);
+  __shared__ uint64_t full[NS], empty[NS];
+  __shared__ float s_lam[32], s_w[32], s_qk[kWarps];
+  __shared__ float s_red[kWarps][DV];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x, b = blockIdx.y, nslot = p.L - 1;
+  const int n = p.pos[b];
+  if (n < 0 || (nslot < 31 && n >= (1 << nslot))) {
+    if (tid == 0) atomicOr(p.status, LLATTN_DEV_DECODE_POS);
+    return;
+  }
+  const unsigned un = (unsigned)n, par = un & 1u;
+  const int m = __ffs(~un) - 1;
+  const size_t bh = (size_t)b * p.H + h;
+  int8_t* codes = p.s.codes + bh * nslot * R::kSlot;
+  uint8_t* exps = p.s.exps + bh * nslot * R::kExps;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      ptx::mbar_init(&full[i], 33);        // the producer's lanes' small copies, and its bulk copy
+      ptx::mbar_init(&empty[i], kWarps);
+    }
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == kWarps) {                    // the producer
+    int i = 0;
+    bool lost = false;
+    for (unsigned u = un; u != 0u; u &= u - 1u, ++i) {
+      const int j = __ffs(u) - 1, st = i % NS;
+      if (i >= NS && !lost && !ptx::mbar_wait(&empty[st], (i / NS - 1) & 1)) {
+        lost = true;
+        atomicOr(p.status, LLATTN_DEV_WAIT_TIMEOUT);
+      }
+      for (int e = lane * 8; e < R::kExps; e += 256)
+        copy8(ptx::smem_u32(s_exps + st * R::kExps + e), exps + (size_t)j * R::kExps + e);
+      arrive_copies(&full[st]);
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&full[st], R::kSlot);
+        ptx::bulk_load(s_codes + st * R::kSlot, codes + (size_t)j * R::kSlot, R::kSlot, &full[st]);
+      }
+      __syncwarp();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+
+  const float la = __ldg(p.log_a + bh);
+  float* gate = p.s.gate + bh * 2 * nslot;
+  if (tid < p.L) s_lam[tid] = __ldg(p.lam + bh * p.L + tid);
+  if (tid < nslot && ((un >> tid) & 1u)) s_w[tid] = expf(gate[par * nslot + tid] + la);
+  const int cc = tid % CPR, r0 = tid / CPR;            // its 16 columns, its first row
+  const Tin* v = static_cast<const Tin*>(p.v) + bh * DV;
+  float qr[R::kRows], kr[R::kRows], qk = 0.f;
+#pragma unroll
+  for (int r = 0; r < R::kRows; ++r) {
+    qr[r] = ld_in(static_cast<const Tin*>(p.q) + bh * DK + r0 + r * (NT / CPR));
+    kr[r] = ld_in(static_cast<const Tin*>(p.k) + bh * DK + r0 + r * (NT / CPR));
+    if (cc == 0) qk = fmaf(qr[r], kr[r], qk);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, o);
+  if (lane == 0) s_qk[warp] = qk;
+  uint64_t carry[R::kRows][8], part[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v0 = ld_in(v + cc * 16 + 2 * i), v1 = ld_in(v + cc * 16 + 2 * i + 1);
+    part[i] = 0ull;
+#pragma unroll
+    for (int r = 0; r < R::kRows; ++r) carry[r][i] = pair(kr[r] * v0, kr[r] * v1);
+  }
+  asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
+
+  int i = 0;
+  bool lost = false;
+  for (unsigned u = un; u != 0u; u &= u - 1u, ++i) {
+    const int j = __ffs(u) - 1, st = i % NS;
+    if (!lost && !ptx::mbar_wait(&full[st], (i / NS) & 1)) {   // reported once; the values are unspecified then
+      lost = true;
+      atomicOr(p.status, LLATTN_DEV_WAIT_TIMEOUT);
+    }
+    const float w = s_w[j], lw = w * s_lam[j + 1];
+#pragma unroll
+    for (int r = 0; r < R::kRows; ++r) {
+      const int row = r0 + r * (NT / CPR);
+      const float sc = q8_scale(s_exps[st * R::kExps + row * NB + (cc >> 1)]);
+      uint64_t x[8];
+      pairs16(*reinterpret_cast<const uint4*>(s_codes + st * R::kSlot + row * DV + cc * 16), x);
+      const float f = qr[r] * sc * lw;
+      const uint64_t f2 = pair(f, f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) part[c] = fma2(f2, x[c], part[c]);
+      if (j < m) {
+        const uint64_t g2 = pair(sc * w, sc * w);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) carry[r][c] = fma2(g2, x[c], carry[r][c]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+  }
+
+  if (m < nslot) {
+#pragma unroll
+    for (int r = 0; r < R::kRows; ++r) {
+      const int row = r0 + r * (NT / CPR);
+      const unsigned e = store_codes(carry[r], codes + (size_t)m * R::kSlot + row * DV + cc * 16);
+      if ((cc & 1) == 0) exps[(size_t)m * R::kExps + row * NB + (cc >> 1)] = (uint8_t)e;
+    }
+  }
+
+  // readout over the warp's 32 / CPR rows, halving the columns a lane carries, then over the warps
+  float x[16];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) unpair(part[c], x[2 * c], x[2 * c + 1]);
+  int first = 0;                           // the lane's first column of its 16
+#pragma unroll
+  for (int o = 16, k = 8; o >= CPR; o >>= 1, k >>= 1) {
+    const bool up = lane & o;
+    if (up) first += k;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (q >= k) break;
+      const float keep = up ? x[q + k] : x[q], send = up ? x[q] : x[q + k];
+      x[q] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < CPR / 2; ++q) s_red[warp][cc * 16 + first + q] = x[q];
+  asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
+  for (int c = tid; c < DV; c += NT) {
+    float s = 0.f, qkt = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      s += s_red[w][c];
+      qkt += s_qk[w];
+    }
+    p.out[bh * DV + c] = fmaf(s_lam[0] * qkt, ld_in(v + c), s);
+  }
+  if (tid < nslot && (((un + 1u) >> tid) & 1u))
+    gate[(par ^ 1u) * nslot + tid] = (tid == m) ? 0.f : gate[par * nslot + tid] + la;
+}
+
+template <typename Tin, int DK, int DV>
+cudaError_t launch_ring(const Q8StepProblem& p, cudaStream_t st) {
+  using R = Ring<DK, DV>;
+  static std::atomic<bool> allowed[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!allowed[dev].load()) {
+    e = cudaFuncSetAttribute(q8_step_ring_kernel<Tin, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
+    if (e != cudaSuccess) return e;
+    allowed[dev].store(true);
+  }
+  q8_step_ring_kernel<Tin, DK, DV><<<dim3(p.H, p.B), R::kThreads + 32, R::kBytes, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename Tin, int DK>
+cudaError_t launch_ring_dk(const Q8StepProblem& p, cudaStream_t st) {
+  switch (p.dv) {
+    case 32: return launch_ring<Tin, DK, 32>(p, st);
+    case 64: return launch_ring<Tin, DK, 64>(p, st);
+    default: return launch_ring<Tin, DK, 128>(p, st);
+  }
+}
+
+constexpr int kRingFrom = 2 * 148;   // (head, sequence) pairs from which they fill the machine
 
 template <typename Tin>
 cudaError_t launch_step(const Q8StepProblem& p, cudaStream_t st) {
+  if ((long long)p.B * p.H >= kRingFrom) {
+    switch (p.dk) {
+      case 32: return launch_ring_dk<Tin, 32>(p, st);
+      case 64: return launch_ring_dk<Tin, 64>(p, st);
+      default: return launch_ring_dk<Tin, 128>(p, st);
+    }
+  }
   const dim3 grid(p.dv / 32, p.H, p.B);
   switch (p.dk) {
     case 32: q8_step_kernel<Tin, 32><<<grid, 64, 0, st>>>(p); break;
@@ -269,50 +548,96 @@ constexpr int pre_smem() {
 }
 
 // One warp's 16 rows of S over the 16 tokens from t0 of a tile: f[2t], f[2t+1], f[2t+8], f[2t+9]
-// scale the lane's tokens.
+// scale the lane's tokens.  The lane's places in a tile (the permutation repeats every 8 tokens)
+// are found once.  Products of one half of f k with all columns come before those of the other, so
+// that no two in a row wait for one another.
+template <typename T, int DK, int DV>
+struct Walker;
+
 template <int DK, int DV>
-__device__ __forceinline__ void step16(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
-                                       const float (&f)[4], int warp, int lane, __nv_bfloat16*) {
-  const int mi = lane >> 3, r = lane & 7;
-  unsigned raw[4], big[4], rest[4];
-  ldmatrix4t(raw, Tile<__nv_bfloat16, DK>::at(ks, t0 + (mi >> 1) * 8 + r, 2 * warp + (mi & 1)));
+struct Walker<__nv_bfloat16, DK, DV> {
+  uint32_t ko, vo[DV / 16];
+  __device__ __forceinline__ Walker(int warp, int lane) {
+    const int mi = lane >> 3, r = lane & 7;
+    ko = Tile<__nv_bfloat16, DK>::at(0u, (mi >> 1) * 8 + r, 2 * warp + (mi & 1));
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    split2(bf16_lo(raw[i]) * f[i & 2], bf16_hi(raw[i]) * f[(i & 2) + 1], big[i], rest[i]);
+    for (int n = 0; n < DV / 16; ++n) vo[n] = Tile<__nv_bfloat16, DV>::at(0u, (mi & 1) * 8 + r, 2 * n + (mi >> 1));
+  }
+  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
+                                       const float (&f)[4]) const {
+    unsigned raw[4], big[4], rest[4], b[DV / 16][4];
+    ldmatrix4t(raw, ks + t0 * (DK * 2) + ko);
 #pragma unroll
-  for (int n = 0; n < DV / 16; ++n) {
-    unsigned b[4];
-    ldmatrix4t(b, Tile<__nv_bfloat16, DV>::at(vs, t0 + (mi & 1) * 8 + r, 2 * n + (mi >> 1)));
+    for (int n = 0; n < DV / 16; ++n) ldmatrix4t(b[n], vs + t0 * (DV * 2) + vo[n]);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      mma_bf16(acc[2 * n + q], big, b[2 * q], b[2 * q + 1]);
-      mma_bf16(acc[2 * n + q], rest, b[2 * q], b[2 * q + 1]);
+    for (int i = 0; i < 4; ++i)
+      split2(bf16_lo(raw[i]) * f[i & 2], bf16_hi(raw[i]) * f[(i & 2) + 1], big[i], rest[i]);
+#pragma unroll
+    for (int n = 0; n < DV / 8; ++n) mma_bf16(acc[n], big, b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+#pragma unroll
+    for (int n = 0; n < DV / 8; ++n) mma_bf16(acc[n], rest, b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+  }
+};
+
+template <int DK, int DV>
+struct Walker<float, DK, DV> {
+  int row, tok;
+  __device__ __forceinline__ Walker(int warp, int lane) : row(16 * warp + (lane >> 2)), tok(2 * (lane & 3)) {}
+  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
+                                       const float (&f)[4]) const {
+    using K = Tile<float, DK>;
+    using V = Tile<float, DV>;
+    const int t = t0 + tok, g = row & 7;   // (the fragment's column has the lane's row within 8)
+    unsigned big[4], rest[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tt = t + (i >> 1) * 8, rr = row + (i & 1) * 8;
+      split2(K::get(ks, tt, rr) * f[i & 2], K::get(ks, tt + 1, rr) * f[(i & 2) + 1], big[i], rest[i]);
+    }
+#pragma unroll
+    for (int n0 = 0; n0 < DV / 8; n0 += 4) {
+      unsigned vb[4][2], vr[4][2];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          split2(V::get(vs, t + 8 * i, 8 * (n0 + n) + g), V::get(vs, t + 8 * i + 1, 8 * (n0 + n) + g), vb[n][i], vr[n][i]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) mma_bf16(acc[n0 + n], big, vb[n][0], vb[n][1]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) mma_bf16(acc[n0 + n], rest, vb[n][0], vb[n][1]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) mma_bf16(acc[n0 + n], big, vr[n][0], vr[n][1]);
     }
   }
-}
-template <int DK, int DV>
-__device__ __forceinline__ void step16(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
-                                       const float (&f)[4], int warp, int lane, float*) {
-  const int g = lane >> 2, t = t0 + 2 * (lane & 3);
-  unsigned big[4], rest[4];
+};
+
+// A thread's share of copying tiles of W-wide rows: a fixed 16-byte piece of every STEP-th token.
+template <typename T, int W, int NT>
+struct Copier {
+  using Tl = Tile<T, W>;
+  static constexpr int STEP = NT / Tl::kPieces, N = STEP < kPreTile ? kPreTile / STEP : 1;
+  static_assert(NT % Tl::kPieces == 0 && (STEP >= kPreTile || kPreTile % STEP == 0), "even shares");
+  int tok, piece;
+  const T* src;            // the thread's piece of the segment's first token
+  size_t stride;           // values from one token to the next
+  __device__ __forceinline__ Copier(const T* base, size_t stride_, int tid)
+      : tok(tid / Tl::kPieces), piece(tid % Tl::kPieces), src(base + piece * (16 / sizeof(T))), stride(stride_) {}
+  // the tile from token t0 of a segment of m tokens that starts at `first`
+  __device__ __forceinline__ void copy(uint32_t dst, int first, int t0, int m) const {
+    if (STEP > kPreTile && tok >= kPreTile) return;
+    const T* from = src + (size_t)(first + t0 + tok) * stride;
+    if (t0 + kPreTile <= m) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 16 * warp + g + (i & 1) * 8, tok = t + (i >> 1) * 8;
-    split2(Tile<float, DK>::get(ks, tok, row) * f[i & 2],
-           Tile<float, DK>::get(ks, tok + 1, row) * f[(i & 2) + 1], big[i], rest[i]);
+      for (int i = 0; i < N; ++i) copy16(Tl::at(dst, tok + i * STEP, piece), from + (size_t)(i * STEP) * stride);
+    } else {
+      for (int i = 0; i < N; ++i) {
+        if (t0 + tok + i * STEP < m) copy16(Tl::at(dst, tok + i * STEP, piece), from + (size_t)(i * STEP) * stride);
+        else zero16(Tl::at(dst, tok + i * STEP, piece));
+      }
+    }
   }
-#pragma unroll
-  for (int n = 0; n < DV / 8; ++n) {
-    unsigned vb[2], vr[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      split2(Tile<float, DV>::get(vs, t + 8 * i, 8 * n + g), Tile<float, DV>::get(vs, t + 8 * i + 1, 8 * n + g),
-             vb[i], vr[i]);
-    mma_bf16(acc[n], big, vb[0], vb[1]);
-    mma_bf16(acc[n], rest, vb[0], vb[1]);
-    mma_bf16(acc[n], big, vr[0], vr[1]);
-  }
-}
+};
 
 // Grid: (head, piece or short level, sequence), heads first: adjacent CTAs read adjacent rows.
 template <typename T, int DK, int DV>
@@ -321,7 +646,8 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
   using K = Tile<T, DK>;
   using V = Tile<T, DV>;
   extern __shared__ float4 pre_smem_raw[];
-  __shared__ float s_f[kPreSeg], s_sum[NT / 32];
+  __shared__ alignas(16) float s_f[kPreSeg];
+  __shared__ float s_sum[NT / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x, b = blockIdx.z, nslot = p.L - 1;
   const SeqSpan sp = seq_span(b, p.T, p.cu_seqlens, p.status);
@@ -353,26 +679,18 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
   for (int i = 0; i < DV / 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  const Walker<T, DK, DV> walk(warp, lane);
+  const Copier<T, DK, NT> kcopy(k, (size_t)p.H * DK, tid);
+  const Copier<T, DV, NT> vcopy(v, (size_t)p.H * DV, tid);
   float D = 0.f;                          // log decay from the segment's end to hi
 
   for (int seg_hi = hi; seg_hi > lo; seg_hi -= kPreSeg) {
     const int seg_lo = max(lo, seg_hi - kPreSeg), m = seg_hi - seg_lo, tiles = (m + kPreTile - 1) / kPreTile;
     auto copy = [&](int tile) {
       if (tile < tiles) {
-        const uint32_t ks = s0 + (tile % kPreStages) * (K::kBytes + V::kBytes), vs = ks + K::kBytes;
-        const int t0 = tile * kPreTile;
-#pragma unroll
-        for (int e = tid; e < kPreTile * K::kPieces; e += NT) {
-          const int tok = e / K::kPieces, c = e % K::kPieces;
-          if (t0 + tok < m) copy16(K::at(ks, tok, c), k + (size_t)(seg_lo + t0 + tok) * p.H * DK + c * (16 / sizeof(T)));
-          else zero16(K::at(ks, tok, c));
-        }
-#pragma unroll
-        for (int e = tid; e < kPreTile * V::kPieces; e += NT) {
-          const int tok = e / V::kPieces, c = e % V::kPieces;
-          if (t0 + tok < m) copy16(V::at(vs, tok, c), v + (size_t)(seg_lo + t0 + tok) * p.H * DV + c * (16 / sizeof(T)));
-          else zero16(V::at(vs, tok, c));
-        }
+        const uint32_t ks = s0 + (tile % kPreStages) * (K::kBytes + V::kBytes);
+        kcopy.copy(ks, seg_lo, tile * kPreTile, m);
+        vcopy.copy(ks + K::kBytes, seg_lo, tile * kPreTile, m);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -415,8 +733,9 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
 #pragma unroll
       for (int t0 = 0; t0 < kPreTile; t0 += 16) {
         const int at = tile * kPreTile + t0 + 2 * (lane & 3);
-        const float f[4] = {s_f[at], s_f[at + 1], s_f[at + 8], s_f[at + 9]};
-        step16<DK, DV>(acc, ks, vs, t0, f, warp, lane, static_cast<T*>(nullptr));
+        const float2 fa = *reinterpret_cast<const float2*>(s_f + at), fb = *reinterpret_cast<const float2*>(s_f + at + 8);
+        const float f[4] = {fa.x, fa.y, fb.x, fb.y};
+        walk.step(acc, ks, vs, t0, f);
       }
     }
   }
@@ -501,6 +820,12 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(Q8PrefillProblem 
   float later = 0.f;                      // log decay of the pieces behind the present ones
   for (int c1 = count; c1 > 0; c1 -= kJoinThreads) {
     const int c0 = max(0, c1 - kJoinThreads), m = c1 - c0;
+    const float4* from = reinterpret_cast<const float4*>(src + (size_t)c0 * size);
+    const size_t step = size / 4;
+    float4 x[8];                          // the last pieces are on their way while weights are made
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < m) x[i] = __ldcs(from + (m - 1 - i) * step);
     __syncthreads();
     if (tid < m) s_w[tid] = logs[first + c0 + tid];
     __syncthreads();
@@ -513,38 +838,46 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(Q8PrefillProblem 
     __syncthreads();
     if (tid < m) s_w[tid] = expf(w);
     __syncthreads();
-#pragma unroll 4
-    for (int c = m - 1; c >= 0; --c) {
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(src + (size_t)(c0 + c) * size));
-      const float f = s_w[c];
-      s.x = fmaf(f, x.x, s.x);
-      s.y = fmaf(f, x.y, s.y);
-      s.z = fmaf(f, x.z, s.z);
-      s.w = fmaf(f, x.w, s.w);
+    for (int c = m - 1; c >= 0; c -= 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i > c) break;
+        const float f = s_w[c - i];
+        s.x = fmaf(f, x[i].x, s.x);
+        s.y = fmaf(f, x[i].y, s.y);
+        s.z = fmaf(f, x[i].z, s.z);
+        s.w = fmaf(f, x[i].w, s.w);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c - 8 - i >= 0) x[i] = __ldcs(from + (c - 8 - i) * step);
     }
   }
   // eight threads hold a block of 32 values
-  const float x[4] = {s.x, s.y, s.z, s.w};
+  const float val[4] = {s.x, s.y, s.z, s.w};
   unsigned top = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(val[i]) & 0x7fffffffu);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   const unsigned e = q8_exp(top);
   const float inv = q8_inverse(e);
   unsigned w = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= (unsigned)(q8_code(x[i], inv, e) & 0xff) << (8 * i);
+  for (int i = 0; i < 4; ++i) w |= (unsigned)(q8_code(val[i], inv, e) & 0xff) << (8 * i);
   const size_t at = (bh * nslot + slot) * size + part * 1024 + tid * 4;
   *reinterpret_cast<unsigned*>(p.s.codes + at) = w;
   if ((tid & 7) == 0) p.s.exps[at / kQ8Block] = (uint8_t)e;
 }
 
-// Tokens of a piece: 512 at least, and as many as keep the pieces of a call at 4096 of 64 x 64
-// values (64 MB of sums).
+// Tokens of a piece: 512, an eighth of whose bytes its sums are; more where the pieces of a call
+// would be over 4096 of 64 x 64 values (64 MB of sums), fewer, 128 at least, where they would leave
+// the machine half empty.
 int piece_log2(int B, int H, int T, int dk, int dv) {
+  const long long bh = (long long)B * H;
   int j = 9;
-  while (j < 24 && (long long)B * H * ((long long)T >> j) * dk * dv > 4096ll * 64 * 64) ++j;
+  while (j > 7 && bh * (T >> j) < 4 * 148) --j;
+  while (j < 24 && bh * (T >> j) * dk * dv > 4096ll * 64 * 64) ++j;
   return j;
 }
 
@@ -612,29 +945,45 @@ __device__ __forceinline__ void store16(__nv_bfloat16* o, const float (&x)[16]) 
   *reinterpret_cast<uint4*>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+constexpr int kReadEach = 4;       // pieces of a thread, asked for together
+
 template <typename Tout>
 __global__ void __launch_bounds__(256) q8_read_kernel(Q8ReadProblem p, long long total) {
   // total = 16-value pieces of the output; per: pieces of one (sequence, head) slot
   const int per = p.dk * p.dv / 16, nslot = p.L - 1;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+  const long long i0 = (long long)blockIdx.x * (256 * kReadEach) + threadIdx.x;
+  uint4 u[kReadEach];
+  unsigned e[kReadEach];
+  long long to[kReadEach];
+#pragma unroll
+  for (int r = 0; r < kReadEach; ++r) {
+    const long long i = i0 + r * 256;
+    to[r] = -1;
+    if (i >= total) continue;
     const long long s = i / per;
     const int piece = (int)(i - s * per);
     long long src = s;
     if (p.slot) {
-      const int b = (int)(s / p.H), j = p.slot[b];
+      const int j = __ldg(p.slot + (int)(s / p.H));
       if (j < 0 || j >= nslot) {
         atomicOr(p.status, LLATTN_DEV_DECODE_POS);
         continue;
       }
       src = s * nslot + j;
     }
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p.s.codes + src * p.dk * p.dv) + piece);
-    const float sc = q8_scale(p.s.exps[src * (p.dk * p.dv / 32) + (piece >> 1)]);
+    u[r] = __ldcs(reinterpret_cast<const uint4*>(p.s.codes + src * p.dk * p.dv) + piece);
+    e[r] = p.s.exps[src * (p.dk * p.dv / 32) + (piece >> 1)];
+    to[r] = i * 16;
+  }
+#pragma unroll
+  for (int r = 0; r < kReadEach; ++r) {
+    if (to[r] < 0) continue;
     float x[16];
-    unpack16(u, x);
+    unpack16(u[r], x);
+    const float sc = q8_scale(e[r]);
 #pragma unroll
     for (int c = 0; c < 16; ++c) x[c] *= sc;
-    store16(static_cast<Tout*>(p.out) + s * p.dk * p.dv + piece * 16, x);
+    store16(static_cast<Tout*>(p.out) + to[r], x);
   }
 }
 
@@ -668,11 +1017,11 @@ cudaError_t q8_read(const Q8ReadProblem& p, cudaStream_t st) {
   const long long slots = (long long)p.B * p.H * (p.slot ? 1 : p.L - 1);
   const long long total = slots * (p.dk * p.dv / 16);
   if (total == 0 || p.L < 2) return cudaSuccess;
-  const long long ctas = (total + 255) / 256;
-  const int grid = (int)(ctas < (1ll << 20) ? ctas : (1ll << 20));
+  const long long each = 256 * kReadEach, grid = (total + each - 1) / each;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   count_launch();
-  if (p.out_dtype == LLATTN_BF16) q8_read_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p, total);
-  else q8_read_kernel<float><<<grid, 256, 0, st>>>(p, total);
+  if (p.out_dtype == LLATTN_BF16) q8_read_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(p, total);
+  else q8_read_kernel<float><<<(unsigned)grid, 256, 0, st>>>(p, total);
   return cudaGetLastError();
 }
 

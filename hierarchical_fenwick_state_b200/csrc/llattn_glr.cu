@@ -192,7 +192,7 @@ struct Shared {
     float P[NT / 32][kCT], H[NT / 32][kCT];
   } map[2];      // a warp may be a tile ahead of another's reading
   float in[kCT];
-  Job job[4];    // a ring: the present tile, the one being copied, the one being taken
+  Job job[4];    // a ring: the present tile, the next, the one being taken
 };
 
 // Joins the threads' maps of a tile (VEC channels of S steps each) over their warps, and the warps'
@@ -329,12 +329,10 @@ __global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch 
       }
     }
   };
-  if (tid == 32) {
-    sh.job[0] = take();
-    sh.job[1] = sh.job[0].k >= 0 ? take() : sh.job[0];
-  }
+  if (tid == 32) sh.job[0] = take();
   __syncthreads();
   copy(sh.job[0]);
+  if (tid == 32) sh.job[1] = sh.job[0].k >= 0 ? take() : sh.job[0];
   for (int it = 0;; ++it) {
     const Job at = sh.job[it & 3];
     if (at.k < 0) break;
@@ -430,12 +428,10 @@ __global__ void __launch_bounds__(NT, MINB) glr_bwd_tiles(GlrBwdProblem p, Scrat
       }
     }
   };
-  if (tid == 32) {
-    sh.job[0] = take();
-    sh.job[1] = sh.job[0].k >= 0 ? take() : sh.job[0];
-  }
+  if (tid == 32) sh.job[0] = take();
   __syncthreads();
   copy(sh.job[0]);
+  if (tid == 32) sh.job[1] = sh.job[0].k >= 0 ? take() : sh.job[0];
   for (int it = 0;; ++it) {
     const Job at = sh.job[it & 3];
     if (at.k < 0) break;

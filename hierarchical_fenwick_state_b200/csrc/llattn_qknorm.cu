@@ -347,7 +347,7 @@ QkBatch batch_of(const QkProblem& p, int turns, int ctas) {
   long long n = (long long)turns * rows / G;
   if (p.rot && n > kQkTable / (p.rot / 2)) n = kQkTable / (p.rot / 2);
   if (n > 4096 / most) n = 4096 / most;
-  if (n > p.N / ctas) n = p.N / ctas;
+  if (n > (p.N + ctas - 1) / ctas) n = (p.N + ctas - 1) / ctas;
   QkBatch b;
   b.tokens = n < 1 ? 1 : (int)n;
   for (int i = 0; i < 2; ++i) b.inv[i] = (unsigned)(((1ull << 32) + p.G[i] - 1) / p.G[i]);

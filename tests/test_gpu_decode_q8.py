@@ -94,6 +94,10 @@ POSITIONS = {
 @pytest.mark.parametrize("H,L,dk,dv,dtype", [
     (3, 14, 64, 64, "bf16"), (2, 17, 128, 128, "bf16"), (5, 5, 32, 32, "f32"), (1, 2, 64, 128, "f32"),
     (2, 14, 128, 32, "bf16"), (4, 5, 32, 128, "bf16"), (1, 32, 32, 32, "f32"),
+    # large batches (296 heads and sequences at least), whose slots go through a ring of 6, 8 or 16
+    (64, 14, 64, 64, "bf16"), (60, 17, 128, 128, "bf16"), (50, 5, 32, 32, "f32"), (100, 2, 64, 128, "f32"),
+    (33, 14, 128, 32, "bf16"), (50, 5, 32, 128, "f32"), (75, 32, 32, 32, "f32"), (33, 14, 64, 32, "f32"),
+    (50, 5, 32, 64, "bf16"), (60, 17, 128, 64, "bf16"),
 ])
 def test_one_step(H, L, dk, dv, dtype):
     pos = torch.tensor(POSITIONS[L], dtype=torch.int32)
