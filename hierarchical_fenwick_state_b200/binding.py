@@ -449,7 +449,7 @@ def _on_device(fn, dev, stream, where, args):
 
 
 def _ptr(t):
-    return t.data_ptr() if t is not None else None
+    return None if t is None else t.data_ptr()
 
 
 def _in_dtype(t) -> int:
@@ -462,71 +462,84 @@ def _in_dtype(t) -> int:
 
 
 def _expect(t, name, dtype, shape, dev, contiguous=True):
-    """Type, device, shape (None: any) and contiguity of an argument that may be absent."""
+    """Type, device, shape (None: any) and contiguity of an argument that may be absent; its
+    address (None where it is absent)."""
     if t is None:
-        return
+        return None
+    if (t.dtype == dtype and t.device == dev and (shape is None or t.shape == shape)
+            and (not contiguous or t.is_contiguous())):
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _expect_state(t, name, n, dev):
+    """The address of a contiguous fp32 tensor of n values that may be absent."""
+    import torch
+    p = _expect(t, name, torch.float32, None, dev)
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold one value for each sequence and channel ({n})")
+    return p
 
 
 def _token_rows(t, name):
     """(tokens, rows per token, d, stride of a token) of a tensor [..., rows, d] whose rows lie
     side by side and whose tokens are one stride apart."""
-    if t.dim() < 3:
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 3:
         raise ValueError(f"{name} must be [..., rows, d]")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    shape, stride = t.shape, t.stride()
     G, d = shape[-2], shape[-1]
-    n = 1
-    for x in shape[:-2]:
-        n *= x
+    if len(shape) == 3:
+        n, step = shape[0], stride[0]
+    else:
+        n, step, span = 1, None, 1   # of the dimensions with more than one entry, the inner ones so far
+        for x, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+            n *= x
+            if x == 1:
+                continue
+            if step is None:
+                step = st
+            elif x and st != step * span:
+                raise ValueError(f"{name}'s tokens must be one stride apart")
+            span *= x
     if n * G * d and (stride[-1] != 1 or (G > 1 and stride[-2] != d)):
         raise ValueError(f"{name}'s rows must lie side by side")
-    step, span = None, 1   # of the dimensions with more than one entry, the inner ones seen so far
-    for x, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
-        if x == 1:
-            continue
-        if step is None:
-            step = st
-        elif n and st != step * span:
-            raise ValueError(f"{name}'s tokens must be one stride apart")
-        span *= x
-    return n, G, d, step if step is not None and n > 1 else G * d
+    return n, G, d, step if n > 1 else G * d
 
 
-def _qk_args(q, k, wq, wk, pos, inv_freq, heads, norm, layout):
+def _qk_args(q, k, wq, wk, pos, inv_freq, norm, layout):
+    """What both directions check and pass: dtype code, tokens, groups, sizes, strides, addresses."""
     import torch
-    dt = _in_dtype(q)
+    dt, dev, f32 = _in_dtype(q), q.device, torch.float32
+    n, Gq, d, qs = _token_rows(q, "q")
+    _, Gk, dk, ks = _token_rows(k, "k")
     if k.dtype != q.dtype:
         raise TypeError("q and k must share a dtype")
-    n, Gq, d, qs = _token_rows(q, "q")
-    nk, Gk, dk, ks = _token_rows(k, "k")
     if k.shape[:-2] != q.shape[:-2] or dk != d:
         raise ValueError("q and k must have the same tokens and row length")
-    dev = q.device
     if k.device != dev:
         raise ValueError(f"k must be on {dev}")
-    _expect(wq, "wq", torch.float32, (d,), dev)
-    _expect(wk, "wk", torch.float32, (d,), dev)
-    rot = 0
+    w = (None if wq is None else _expect(wq, "wq", f32, (d,), dev),
+         None if wk is None else _expect(wk, "wk", f32, (d,), dev))
+    rot, at, freq = 0, None, None
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _expect(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev)
+        freq = _expect(inv_freq, "inv_freq", f32, (rot // 2,), dev)
         if pos is None:
             raise ValueError("a rotation needs pos")
-        _expect(pos, "pos", torch.int32, None, dev)
         if pos.numel() != n:
             raise ValueError("pos must have one entry for each token")
+        at = _expect(pos, "pos", torch.int32, None, dev)
     if norm not in NORMS or layout not in LAYOUTS:
         raise ValueError(f"norm is one of {tuple(NORMS)}, layout one of {tuple(LAYOUTS)}")
-    return dt, n, Gq, Gk, d, qs, ks, rot, heads if heads is not None else max(Gq, Gk)
+    return dt, dev, n, Gq, Gk, d, rot, (q.data_ptr(), k.data_ptr(), qs, ks, *w, at, freq)
 
 
 def qk_norm_rope(q, k, *, wq=None, wk=None, pos=None, inv_freq=None, heads: Optional[int] = None,
@@ -537,19 +550,16 @@ def qk_norm_rope(q, k, *, wq=None, wk=None, pos=None, inv_freq=None, heads: Opti
     apart (slices of a projection's output do).  heads: rows each token has in the outputs
     [..., heads, d] (default: the larger of Gq, Gk); each group is written to heads / G of them.
     wq, wk fp32 [d]; inv_freq fp32 [rot/2] with pos int32, one entry per token, or None."""
-    import torch
-    dt, n, Gq, Gk, d, qs, ks, rot, H = _qk_args(q, k, wq, wk, pos, inv_freq, heads, norm, layout)
-    dev, shape = q.device, q.shape[:-2] + (H, d)
+    dt, dev, n, Gq, Gk, d, rot, args = _qk_args(q, k, wq, wk, pos, inv_freq, norm, layout)
+    H = max(Gq, Gk) if heads is None else heads
+    shape = q.shape[:-2] + (H, d)
     if out is None:
-        out = (torch.empty(shape, dtype=q.dtype, device=dev),
-               torch.empty(shape, dtype=q.dtype, device=dev))
+        out = (q.new_empty(shape), q.new_empty(shape))
+        o = (out[0].data_ptr(), out[1].data_ptr())
     else:
-        _expect(out[0], "out[0]", q.dtype, shape, dev)
-        _expect(out[1], "out[1]", q.dtype, shape, dev)
+        o = (_expect(out[0], "out[0]", q.dtype, shape, dev), _expect(out[1], "out[1]", q.dtype, shape, dev))
     _on_device(lib().llattn_qk_norm_rope, dev, stream, "llattn_qk_norm_rope",
-               (dt, _ptr(q), _ptr(k), qs, ks, _ptr(wq), _ptr(wk), _ptr(pos) if rot else None,
-                _ptr(inv_freq), _ptr(out[0]), _ptr(out[1]), n, Gq, Gk, H, d, rot,
-                LAYOUTS[layout], NORMS[norm], eps))
+               (dt, *args, *o, n, Gq, Gk, H, d, rot, LAYOUTS[layout], NORMS[norm], eps))
     return out
 
 
@@ -560,33 +570,33 @@ def qk_norm_rope_backward(q, k, dqo, dko, *, wq=None, wk=None, pos=None, inv_fre
 
     q, k, wq, wk, pos, inv_freq, norm, layout, eps as in the forward; dqo, dko fp32
     [..., heads, d].  Returns a dict of fp32 tensors q, k and, where weights are given, wq, wk (or
-    fills `grads`, a dict of preallocated ones; its q and k may be strided as the inputs may)."""
+    fills `grads`, a dict of preallocated ones; its q and k may be strided as the inputs may).
+    workspace: qk_norm_rope_bwd_workspace_bytes(d) bytes, or None for torch's."""
     import torch
-    heads = dqo.shape[-2] if dqo.dim() >= 3 else None
-    dt, n, Gq, Gk, d, qs, ks, rot, H = _qk_args(q, k, wq, wk, pos, inv_freq, heads, norm, layout)
-    dev, f32 = q.device, torch.float32
-    _expect(dqo, "dqo", f32, q.shape[:-2] + (H, d), dev)
-    _expect(dko, "dko", f32, q.shape[:-2] + (H, d), dev)
+    dt, dev, n, Gq, Gk, d, rot, args = _qk_args(q, k, wq, wk, pos, inv_freq, norm, layout)
+    if dqo.dim() < 3:
+        raise ValueError("dqo must be [..., heads, d]")
+    f32, H = torch.float32, dqo.shape[-2]
+    shape = q.shape[:-2] + (H, d)
+    dy = (_expect(dqo, "dqo", f32, shape, dev), _expect(dko, "dko", f32, shape, dev))
     if grads is None:
-        grads = {"q": torch.empty(q.shape, dtype=f32, device=dev),
-                 "k": torch.empty(k.shape, dtype=f32, device=dev)}
+        grads = {"q": dqo.new_empty(q.shape), "k": dqo.new_empty(k.shape)}
         if wq is not None:
-            grads["wq"] = torch.empty(d, dtype=f32, device=dev)
+            grads["wq"] = torch.empty_like(wq)
         if wk is not None:
-            grads["wk"] = torch.empty(d, dtype=f32, device=dev)
+            grads["wk"] = torch.empty_like(wk)
         dqs, dks = Gq * d, Gk * d
     else:
         _expect(grads["q"], "grads['q']", f32, q.shape, dev, contiguous=False)
         _expect(grads["k"], "grads['k']", f32, k.shape, dev, contiguous=False)
-        _expect(grads.get("wq"), "grads['wq']", f32, (d,), dev)
-        _expect(grads.get("wk"), "grads['wk']", f32, (d,), dev)
         dqs, dks = _token_rows(grads["q"], "grads['q']")[3], _token_rows(grads["k"], "grads['k']")[3]
-    ws_n = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    dw = (_expect(grads.get("wq"), "grads['wq']", f32, (d,), dev),
+          _expect(grads.get("wk"), "grads['wk']", f32, (d,), dev))
+    need = qk_norm_rope_bwd_workspace_bytes(d) if dw[0] or dw[1] else 0
+    ws, ws_n = _workspace(workspace, need, dev, stream)
     _on_device(lib().llattn_qk_norm_rope_bwd, dev, stream, "llattn_qk_norm_rope_bwd",
-               (dt, _ptr(q), _ptr(k), qs, ks, _ptr(wq), _ptr(wk), _ptr(pos) if rot else None,
-                _ptr(inv_freq), _ptr(dqo), _ptr(dko), _ptr(grads["q"]), _ptr(grads["k"]), dqs, dks,
-                _ptr(grads.get("wq")), _ptr(grads.get("wk")), n, Gq, Gk, H, d, rot,
-                LAYOUTS[layout], NORMS[norm], eps, _ptr(workspace), ws_n))
+               (dt, *args, *dy, grads["q"].data_ptr(), grads["k"].data_ptr(), dqs, dks, *dw, n, Gq,
+                Gk, H, d, rot, LAYOUTS[layout], NORMS[norm], eps, _ptr(ws), ws_n))
     return grads
 
 
@@ -599,22 +609,24 @@ def qk_norm_rope_bwd_workspace_bytes(d: int, weights: bool = True) -> int:
 
 def _glr_shape(t, cu_seqlens, T):
     """(B, T, D) of [B, T, ...channels], or [total, ...channels] with cu_seqlens."""
-    import torch
     if not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
+    shape = t.shape
     if cu_seqlens is None:
-        if t.dim() < 3:
+        if len(shape) < 3:
             raise ValueError("dense inputs are [B, T, ...channels]")
-        B, T, rest = t.shape[0], t.shape[1], t.shape[2:]
+        B, T, D = shape[0], shape[1], shape[2]
+        rest = shape[3:]
     else:
-        _expect(cu_seqlens, "cu_seqlens", torch.int32, None, t.device)
         if T is None:
             raise ValueError("packed inputs need T (the bound on every length)")
-        if t.dim() < 2 or cu_seqlens.numel() < 1:
+        if len(shape) < 2 or cu_seqlens.numel() < 1:
             raise ValueError("packed inputs are [total, ...channels] with cu_seqlens [B + 1]")
-        B, rest = cu_seqlens.numel() - 1, t.shape[1:]
-        T = T if t.shape[0] else 0   # no rows at all: every sequence is empty
-    return B, T, rest.numel(), (B,) + tuple(rest)
+        B, D, rest = cu_seqlens.numel() - 1, shape[1], shape[2:]
+        T = T if shape[0] else 0   # no rows at all: every sequence is empty
+    for x in rest:
+        D *= x
+    return B, T, D
 
 
 def glr_workspace_bytes(B: int, T: int, D: int) -> int:
@@ -623,6 +635,11 @@ def glr_workspace_bytes(B: int, T: int, D: int) -> int:
     _check(lib().llattn_glr_workspace_bytes(int(B), int(T), int(D), ctypes.byref(n)),
            "llattn_glr_workspace_bytes")
     return int(n.value)
+
+
+def _glr_need(B, T, D):
+    """glr_workspace_bytes without the call (sizes that it refuses are refused by the operator)."""
+    return 0 if T <= 64 or B == 0 or D == 0 else 256 + -(-T // 64) * B * -(-D // 32) * 512
 
 
 def _workspace(workspace, need, dev, stream):
@@ -644,25 +661,22 @@ def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[
 
     x bf16 or fp32 and log_a fp32, both [B, T, ...channels], or [total, ...channels] with
     cu_seqlens and T.  h0 [B, ...channels] fp32 is the state carried in; h_last, a preallocated
-    tensor of the same shape (h0 itself will do), receives the state after the last token."""
+    tensor of the same shape (h0 itself will do), receives the state after the last token.
+    workspace: glr_workspace_bytes() bytes, or None for torch's."""
     import torch
-    dt, (B, T, D, state) = _in_dtype(x), _glr_shape(x, cu_seqlens, T)
+    dt, (B, T, D) = _in_dtype(x), _glr_shape(x, cu_seqlens, T)
     dev, f32 = x.device, torch.float32
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    _expect(log_a, "log_a", f32, x.shape, dev)
-    for t, n in ((h0, "h0"), (h_last, "h_last")):
-        _expect(t, n, f32, None, dev)
-        if t is not None and t.numel() != B * D:
-            raise ValueError(f"{n} must have shape {state}")
+    la = _expect(log_a, "log_a", f32, x.shape, dev)
+    states = _expect_state(h0, "h0", B * D, dev), _expect_state(h_last, "h_last", B * D, dev)
+    cu = _expect(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=f32, device=dev)
-    else:
-        _expect(out, "out", f32, x.shape, dev)
-    ws, ws_n = _workspace(workspace, glr_workspace_bytes(B, T, D), dev, stream)
+        out = torch.empty_like(log_a)
+    h = _expect(out, "out", f32, x.shape, dev)
+    ws, ws_n = _workspace(workspace, _glr_need(B, T, D), dev, stream)
     _on_device(lib().llattn_glr_fwd, dev, stream, "llattn_glr_fwd",
-               (dt, _ptr(x), _ptr(log_a), _ptr(h0), _ptr(out), _ptr(h_last), B, T, D,
-                _ptr(cu_seqlens), _ptr(ws), ws_n))
+               (dt, x.data_ptr(), la, states[0], h, states[1], B, T, D, cu, _ptr(ws), ws_n))
     return out
 
 
@@ -674,32 +688,23 @@ def glr_backward(log_a, h, dh, *, h0=None, dh_last=None, cu_seqlens=None, T: Opt
     [B, ...channels] or None.  Returns a dict of fp32 tensors x, log_a and, where h0 is given, h0
     (or fills `grads`, a dict of preallocated ones)."""
     import torch
-    B, T, D, state = _glr_shape(log_a, cu_seqlens, T)
+    B, T, D = _glr_shape(log_a, cu_seqlens, T)
     dev, f32 = log_a.device, torch.float32
-    _expect(log_a, "log_a", f32, None, dev)
-    _expect(h, "h", f32, log_a.shape, dev)
-    _expect(dh, "dh", f32, log_a.shape, dev)
-    for t, n in ((h0, "h0"), (dh_last, "dh_last")):
-        _expect(t, n, f32, None, dev)
-        if t is not None and t.numel() != B * D:
-            raise ValueError(f"{n} must have shape {state}")
+    shape = log_a.shape
+    ins = (_expect(log_a, "log_a", f32, None, dev), _expect(h, "h", f32, shape, dev),
+           _expect_state(h0, "h0", B * D, dev), _expect(dh, "dh", f32, shape, dev),
+           _expect_state(dh_last, "dh_last", B * D, dev))
+    cu = _expect(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
     if grads is None:
-        grads = {"x": torch.empty(log_a.shape, dtype=f32, device=dev),
-                 "log_a": torch.empty(log_a.shape, dtype=f32, device=dev)}
+        grads = {"x": torch.empty_like(log_a), "log_a": torch.empty_like(log_a)}
         if h0 is not None:
-            grads["h0"] = torch.empty(h0.shape, dtype=f32, device=dev)
-    else:
-        _expect(grads["x"], "grads['x']", f32, log_a.shape, dev)
-        _expect(grads["log_a"], "grads['log_a']", f32, log_a.shape, dev)
-        t = grads.get("h0")
-        _expect(t, "grads['h0']", f32, None, dev)
-        if t is not None and t.numel() != B * D:
-            raise ValueError(f"grads['h0'] must have shape {state}")
-    ws, ws_n = _workspace(workspace, glr_workspace_bytes(B, T, D), dev, stream)
+            grads["h0"] = torch.empty_like(h0)
+    outs = (_expect(grads["x"], "grads['x']", f32, shape, dev),
+            _expect(grads["log_a"], "grads['log_a']", f32, shape, dev),
+            _expect_state(grads.get("h0"), "grads['h0']", B * D, dev))
+    ws, ws_n = _workspace(workspace, _glr_need(B, T, D), dev, stream)
     _on_device(lib().llattn_glr_bwd, dev, stream, "llattn_glr_bwd",
-               (_ptr(log_a), _ptr(h), _ptr(h0), _ptr(dh), _ptr(dh_last), _ptr(grads["x"]),
-                _ptr(grads["log_a"]), _ptr(grads.get("h0")), B, T, D, _ptr(cu_seqlens), _ptr(ws),
-                ws_n))
+               (*ins, *outs, B, T, D, cu, _ptr(ws), ws_n))
     return grads
 
 
@@ -726,16 +731,12 @@ def decode_step_q8(q, k, v, log_a, lam, pos, state, out, B, H, L, dk, dv, stream
     fp32, pos int32 [B], out fp32 [B,H,dv]."""
     import torch
     dt, dev, f32 = _in_dtype(q), _q8_state(state, B, H, L, dk, dv), torch.float32
-    _expect(q, "q", q.dtype, (B, H, dk), dev)
-    _expect(k, "k", q.dtype, (B, H, dk), dev)
-    _expect(v, "v", q.dtype, (B, H, dv), dev)
-    _expect(log_a, "log_a", f32, (B, H), dev)
-    _expect(lam, "lam", f32, (B, H, L), dev)
-    _expect(pos, "pos", torch.int32, (B,), dev)
-    _expect(out, "out", f32, (B, H, dv), dev)
+    t, key, val = q.dtype, (B, H, dk), (B, H, dv)
+    args = (_expect(q, "q", t, key, dev), _expect(k, "k", t, key, dev), _expect(v, "v", t, val, dev),
+            _expect(log_a, "log_a", f32, (B, H), dev), _expect(lam, "lam", f32, (B, H, L), dev),
+            _expect(pos, "pos", torch.int32, (B,), dev), state.data_ptr(), _expect(out, "out", f32, val, dev))
     _on_device(lib().llattn_decode_step_q8, dev, stream, "llattn_decode_step_q8",
-               (dt, _ptr(q), _ptr(k), _ptr(v), _ptr(log_a), _ptr(lam), _ptr(pos), _ptr(state),
-                _ptr(out), B, H, L, dk, dv))
+               (dt, *args, B, H, L, dk, dv))
     return out
 
 
@@ -751,18 +752,19 @@ def prefill_q8_workspace_bytes(B: int, H: int, T: int, L: int, dk: int, dv: int)
 def prefill_state_q8(k, v, log_a, state, B, H, T, L, dk, dv, cu_seqlens=None, workspace=None,
                      stream=None):
     """llattn_prefill_state_q8: prefill_state into the 8-bit state.  k, v dense [B,T,H,d] or packed
-    [total,H,d] (bf16 or fp32), log_a fp32 [..,H], cu_seqlens int32 [B+1] or None."""
+    [total,H,d] (bf16 or fp32), log_a fp32 [..,H], cu_seqlens int32 [B+1] or None.  workspace:
+    prefill_q8_workspace_bytes() bytes, or None for torch's."""
     import torch
-    dt, dev = _in_dtype(k), _q8_state(state, B, H, L, dk, dv)
+    dt, dev, t = _in_dtype(k), _q8_state(state, B, H, L, dk, dv), k.dtype
     lead = (B, T) if cu_seqlens is None else (k.shape[0],)
-    _expect(k, "k", k.dtype, lead + (H, dk), dev)
-    _expect(v, "v", k.dtype, lead + (H, dv), dev)
-    _expect(log_a, "log_a", torch.float32, lead + (H,), dev)
-    _expect(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    args = (_expect(k, "k", t, lead + (H, dk), dev), _expect(v, "v", t, lead + (H, dv), dev),
+            _expect(log_a, "log_a", torch.float32, lead + (H,), dev), state.data_ptr())
+    cu = _expect(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    if cu is not None and k.shape[0] == 0:
+        T = 0                        # no rows at all: every sequence is empty
     ws, ws_n = _workspace(workspace, prefill_q8_workspace_bytes(B, H, T, L, dk, dv), dev, stream)
     _on_device(lib().llattn_prefill_state_q8, dev, stream, "llattn_prefill_state_q8",
-               (dt, _ptr(k), _ptr(v), _ptr(log_a), _ptr(state), B, H, T, L, dk, dv,
-                _ptr(cu_seqlens), _ptr(ws), ws_n))
+               (dt, *args, B, H, T, L, dk, dv, cu, _ptr(ws), ws_n))
     return state
 
 
@@ -771,12 +773,11 @@ def read_state_q8(state, B, H, L, dk, dv, slot=None, out=None, dtype=None, strea
     [B]) those of one slot of each sequence, [B,H,dk,dv]; bf16 (the default) and fp32 are exact."""
     import torch
     dev = _q8_state(state, B, H, L, dk, dv)
-    _expect(slot, "slot", torch.int32, (B,), dev)
+    at = _expect(slot, "slot", torch.int32, (B,), dev)
     shape = (B, H, dk, dv) if slot is not None else (B, H, L - 1, dk, dv)
     if out is None:
-        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
-    else:
-        _expect(out, "out", out.dtype, shape, dev)
+        out = state.new_empty(shape, dtype=dtype or torch.bfloat16)
+    o = _expect(out, "out", out.dtype, shape, dev)
     _on_device(lib().llattn_read_state_q8, dev, stream, "llattn_read_state_q8",
-               (_ptr(state), _ptr(slot), _ptr(out), _in_dtype(out), B, H, L, dk, dv))
+               (state.data_ptr(), at, o, _in_dtype(out), B, H, L, dk, dv))
     return out

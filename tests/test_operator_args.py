@@ -112,6 +112,8 @@ def test_glr_backward_refusals(kw, status):
 def test_glr_workspace():
     assert binding.glr_workspace_bytes(64, 1, 2048) == 0
     assert binding.glr_workspace_bytes(0, 5000, 64) == 0
+    for shape in ((1, 64, 7), (1, 65, 7), (64, 1, 2048), (3, 1000, 33), (0, 100, 4), (5, 16384, 1024)):
+        assert binding.glr_workspace_bytes(*shape) == binding._glr_need(*shape), shape
     n = binding.glr_workspace_bytes(1, 65536, 2048)
     assert 0 < n < 65536 * 2048      # small beside the 10 bytes per element of a call
     for bad in ((-1, 1, 1), (1, 1 << 25, 1), (1, 1, 65536), (65535, 1 << 24, 64)):
