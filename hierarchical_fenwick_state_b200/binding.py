@@ -448,10 +448,6 @@ def _on_device(fn, dev, stream, where, args):
         raise LLAttnError(st, where)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _in_dtype(t) -> int:
     import torch
     if t.dtype == torch.bfloat16:
@@ -592,11 +588,11 @@ def qk_norm_rope_backward(q, k, dqo, dko, *, wq=None, wk=None, pos=None, inv_fre
         dqs, dks = _token_rows(grads["q"], "grads['q']")[3], _token_rows(grads["k"], "grads['k']")[3]
     dw = (_expect(grads.get("wq"), "grads['wq']", f32, (d,), dev),
           _expect(grads.get("wk"), "grads['wk']", f32, (d,), dev))
-    need = qk_norm_rope_bwd_workspace_bytes(d) if dw[0] or dw[1] else 0
-    ws, ws_n = _workspace(workspace, need, dev, stream)
+    need = 148 * 2 * 2 * d * 4 if dw[0] or dw[1] else 0   # as qk_norm_rope_bwd_workspace_bytes
+    ws, at, size = _workspace(workspace, need, dqo, stream)
     _on_device(lib().llattn_qk_norm_rope_bwd, dev, stream, "llattn_qk_norm_rope_bwd",
                (dt, *args, *dy, grads["q"].data_ptr(), grads["k"].data_ptr(), dqs, dks, *dw, n, Gq,
-                Gk, H, d, rot, LAYOUTS[layout], NORMS[norm], eps, _ptr(ws), ws_n))
+                Gk, H, d, rot, LAYOUTS[layout], NORMS[norm], eps, at, size))
     return grads
 
 
@@ -642,17 +638,20 @@ def _glr_need(B, T, D):
     return 0 if T <= 64 or B == 0 or D == 0 else 256 + -(-T // 64) * B * -(-D // 32) * 512
 
 
-def _workspace(workspace, need, dev, stream):
-    """A call's scratch: the caller's, or torch's for this call alone (none where none is needed)."""
+def _workspace(workspace, need, like, stream):
+    """A call's scratch: the caller's, or torch's for this call alone (none where none is needed):
+    (tensor, address, bytes).  like: an fp32 tensor on the call's device."""
     import torch
     if workspace is not None:
-        return workspace, workspace.numel() * workspace.element_size()
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need == 0:
-        return None, 0
+        return None, None, 0
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev), need
-    with torch.cuda.stream(stream):   # torch hands it on in that stream's order
-        return torch.empty(need, dtype=torch.uint8, device=dev), need
+        ws = like.new_empty(need // 4)
+    else:
+        with torch.cuda.stream(stream):   # torch hands it on in that stream's order
+            ws = like.new_empty(need // 4)
+    return ws, ws.data_ptr(), need
 
 
 def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[int] = None,
@@ -674,9 +673,9 @@ def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[
     if out is None:
         out = torch.empty_like(log_a)
     h = _expect(out, "out", f32, x.shape, dev)
-    ws, ws_n = _workspace(workspace, _glr_need(B, T, D), dev, stream)
+    ws, at, size = _workspace(workspace, _glr_need(B, T, D), log_a, stream)
     _on_device(lib().llattn_glr_fwd, dev, stream, "llattn_glr_fwd",
-               (dt, x.data_ptr(), la, states[0], h, states[1], B, T, D, cu, _ptr(ws), ws_n))
+               (dt, x.data_ptr(), la, states[0], h, states[1], B, T, D, cu, at, size))
     return out
 
 
@@ -702,9 +701,9 @@ def glr_backward(log_a, h, dh, *, h0=None, dh_last=None, cu_seqlens=None, T: Opt
     outs = (_expect(grads["x"], "grads['x']", f32, shape, dev),
             _expect(grads["log_a"], "grads['log_a']", f32, shape, dev),
             _expect_state(grads.get("h0"), "grads['h0']", B * D, dev))
-    ws, ws_n = _workspace(workspace, _glr_need(B, T, D), dev, stream)
+    ws, at, size = _workspace(workspace, _glr_need(B, T, D), log_a, stream)
     _on_device(lib().llattn_glr_bwd, dev, stream, "llattn_glr_bwd",
-               (*ins, *outs, B, T, D, cu, _ptr(ws), ws_n))
+               (*ins, *outs, B, T, D, cu, at, size))
     return grads
 
 
@@ -762,9 +761,9 @@ def prefill_state_q8(k, v, log_a, state, B, H, T, L, dk, dv, cu_seqlens=None, wo
     cu = _expect(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
     if cu is not None and k.shape[0] == 0:
         T = 0                        # no rows at all: every sequence is empty
-    ws, ws_n = _workspace(workspace, prefill_q8_workspace_bytes(B, H, T, L, dk, dv), dev, stream)
+    ws, at, size = _workspace(workspace, prefill_q8_workspace_bytes(B, H, T, L, dk, dv), log_a, stream)
     _on_device(lib().llattn_prefill_state_q8, dev, stream, "llattn_prefill_state_q8",
-               (dt, *args, B, H, T, L, dk, dv, cu, _ptr(ws), ws_n))
+               (dt, *args, B, H, T, L, dk, dv, cu, at, size))
     return state
 
 

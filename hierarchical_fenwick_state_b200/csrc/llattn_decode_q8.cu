@@ -55,12 +55,6 @@ __device__ __forceinline__ int q8_code(float x, float inv, unsigned e) {
 
 constexpr int kStepVals = 16;   // adjacent codes per thread: one 16-byte load
 
-__device__ __forceinline__ void unpack16(const uint4& u, float (&x)[16]) {
-  const unsigned w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = (float)(int)(signed char)(w[i >> 2] >> (8 * (i & 3)));
-}
-
 // Pairs of fp32 in one register pair: one instruction for two sums or products.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t r;
@@ -95,6 +89,24 @@ __device__ __forceinline__ void pairs16(const uint4& u, uint64_t (&x)[8]) {
   }
 }
 
+__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(p) + i);
+    x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
+  }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const unsigned w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[8 * i + j] = __uint_as_float((j & 1) ? (w[j >> 1] & 0xffff0000u) : (w[j >> 1] << 16));
+  }
+}
+
 // Sixteen values, a block's half beside its other half on the neighbouring lane, as codes; returns
 // the block's exponent code.
 __device__ __forceinline__ unsigned store_codes(const uint64_t (&v)[8], int8_t* to) {
@@ -102,13 +114,24 @@ __device__ __forceinline__ unsigned store_codes(const uint64_t (&v)[8], int8_t* 
   unsigned top = 0u, w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int c = 0; c < 8; ++c) unpair(v[c], x[2 * c], x[2 * c + 1]);
+  float t = 0.f;
 #pragma unroll
-  for (int c = 0; c < 16; ++c) top = max(top, __float_as_uint(x[c]) & 0x7fffffffu);
+  for (int c = 0; c < 16; ++c)             // (the maximum that keeps NaN)
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(t) : "f"(fabsf(x[c])));
+  top = __float_as_uint(t) & 0x7fffffffu;
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   const unsigned e = q8_exp(top);
   const float inv = q8_inverse(e);
+  // x / 2^e is exact, and added to 1.5 * 2^23 it is rounded to a whole number, ties to even, whose
+  // last byte is the code
 #pragma unroll
-  for (int c = 0; c < 16; ++c) w[c >> 2] |= (unsigned)(q8_code(x[c], inv, e) & 0xff) << (8 * (c & 3));
+  for (int c = 0; c < 16; c += 4) {
+    unsigned r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(fmaf(x[c + i], inv, 12582912.f));
+    const unsigned lo = __byte_perm(r[0], r[1], 0x0040), hi = __byte_perm(r[2], r[3], 0x0040);
+    w[c >> 2] = e == 255u ? 0u : __byte_perm(lo, hi, 0x5410);
+  }
   *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
   return e;
 }
@@ -163,10 +186,14 @@ __global__ void __launch_bounds__(2 * DK, 640 / (2 * DK)) q8_step_kernel(Q8StepP
   const float kr = ld_in(static_cast<const Tin*>(p.k) + bh * DK + r);
   const Tin* v = static_cast<const Tin*>(p.v) + bh * p.dv + col;
   uint64_t carry[8], part[8];
+  {
+    float vv[16];
+    load16(v, vv);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    carry[i] = pair(kr * ld_in(v + 2 * i), kr * ld_in(v + 2 * i + 1));
-    part[i] = 0ull;
+    for (int i = 0; i < 8; ++i) {
+      carry[i] = pair(kr * vv[2 * i], kr * vv[2 * i + 1]);
+      part[i] = 0ull;
+    }
   }
   float qk = half ? 0.f : qr * kr;
 #pragma unroll
@@ -235,16 +262,16 @@ __global__ void __launch_bounds__(2 * DK, 640 / (2 * DK)) q8_step_kernel(Q8StepP
 
 // ---- the step of a large batch ----
 //
-// One CTA per (head, sequence) there: a whole slot is one run of dk * dv bytes, so a producer warp
-// copies the occupied slots, lowest first, into a ring in shared memory (a bulk copy each, the
-// block exponents beside it), and the other warps read them out.  Bytes in flight wait in shared
-// memory in place of registers, which lets six CTAs of 64 x 64 states share an SM.
+// One CTA per (head, sequence) there: a whole slot is one run of dk * dv bytes, so one warp copies
+// the occupied slots, lowest first, to shared memory (a bulk copy each, the block exponents beside
+// it), kStages at a time, and the other warps read them out.  Bytes in flight wait in shared memory
+// in place of registers, which lets six CTAs of 64 x 64 states share an SM.
 template <int DK, int DV>
 struct Ring {
   static constexpr int kSlot = DK * DV, kExps = DK * (DV / 32);
   static constexpr int kStages = kSlot <= 2048 ? 16 : kSlot <= 8192 ? 8 : 6;
   static constexpr int kChunks = kSlot / 16;
-  static constexpr int kThreads = kChunks <= 64 ? 64 : kChunks / 2 < 64 ? 64 : kChunks / 2;   // readers
+  static constexpr int kThreads = kChunks / 2 < 64 ? 64 : kChunks / 2;   // readers
   static constexpr int kRows = kChunks / kThreads;         // rows of a reader, 16 columns of each
   static constexpr int kBytes = kStages * (kSlot + kExps);
 };
@@ -256,125 +283,107 @@ __device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
 __device__ __forceinline__ void arrive_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
-}
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(Ring<DK, DV>::kThreads + 32) q8_step_ring_kernel(Q8StepProblem p) {
+__global__ void __launch_bounds__(Ring<DK, DV>::kThreads + 32, Ring<DK, DV>::kThreads == 128 ? 6 : 1) q8_step_ring_kernel(Q8StepProblem p) {
   using R = Ring<DK, DV>;
   constexpr int NT = R::kThreads, kWarps = NT / 32, CPR = DV / 16, NB = DV / 32, NS = R::kStages;
   extern __shared__ float4 ring_smem[];
   int8_t* s_codes = reinterpret_cast<int8_t*>(ring_smem);
   uint8_t* s_exps = reinterpret_cast<uint8_t*>(s_codes + NS * R::kSlot);
-  __shared__ uint64_t full[NS], empty[NS];
+  __shared__ uint64_t full;                // a batch of slots has come
   __shared__ float s_lam[32], s_w[32], s_qk[kWarps];
   __shared__ float s_red[kWarps][DV];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x, b = blockIdx.y, nslot = p.L - 1;
-  const int n = p.pos[b];
+  const int n = __ldg(p.pos + b);
+  const size_t bh = (size_t)b * p.H + h;
+  int8_t* codes = p.s.codes + bh * nslot * R::kSlot;
+  uint8_t* exps = p.s.exps + bh * nslot * R::kExps;
+  const int cc = tid % CPR, r0 = tid / CPR;            // a reader's 16 columns, its first row
+  const Tin* v = static_cast<const Tin*>(p.v) + bh * DV;
+  float qr[R::kRows], kr[R::kRows], la = 0.f, lam = 0.f;
+  if (warp < kWarps) {                     // on their way beside the position
+#pragma unroll
+    for (int r = 0; r < R::kRows; ++r) {
+      qr[r] = ld_in(static_cast<const Tin*>(p.q) + bh * DK + r0 + r * (NT / CPR));
+      kr[r] = ld_in(static_cast<const Tin*>(p.k) + bh * DK + r0 + r * (NT / CPR));
+    }
+    la = __ldg(p.log_a + bh);
+    if (tid < p.L) lam = __ldg(p.lam + bh * p.L + tid);
+  } else {
+    if (lane == 0) {
+      ptx::mbar_init(&full, 33);           // the copying lanes' small copies, and the bulk copies
+      ptx::fence_mbar_init();
+    }
+    __syncwarp();
+  }
   if (n < 0 || (nslot < 31 && n >= (1 << nslot))) {
     if (tid == 0) atomicOr(p.status, LLATTN_DEV_DECODE_POS);
     return;
   }
   const unsigned un = (unsigned)n, par = un & 1u;
-  const int m = __ffs(~un) - 1;
-  const size_t bh = (size_t)b * p.H + h;
-  int8_t* codes = p.s.codes + bh * nslot * R::kSlot;
-  uint8_t* exps = p.s.exps + bh * nslot * R::kExps;
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      ptx::mbar_init(&full[i], 33);        // the producer's lanes' small copies, and its bulk copy
-      ptx::mbar_init(&empty[i], kWarps);
-    }
-    ptx::fence_mbar_init();
-  }
-  __syncthreads();
+  const int m = __ffs(~un) - 1, cnt = __popc(un);
 
-  if (warp == kWarps) {                    // the producer
-    int i = 0;
-    bool lost = false;
-    for (unsigned u = un; u != 0u; u &= u - 1u, ++i) {
-      const int j = __ffs(u) - 1, st = i % NS;
-      if (i >= NS && !lost && !ptx::mbar_wait(&empty[st], (i / NS - 1) & 1)) {
-        lost = true;
-        atomicOr(p.status, LLATTN_DEV_WAIT_TIMEOUT);
+  if (warp == kWarps) {                    // the copying warp
+    unsigned u = un;
+    for (int left = cnt, batch = 0; left > 0 || batch == 0; left -= NS, ++batch) {
+      const int k = left < NS ? left : NS;
+      if (batch > 0)                       // the batch before is read (the readers' side: below)
+        asm volatile("bar.sync 3, %0;" ::"n"(NT + 32) : "memory");
+      if (lane == 0) ptx::mbar_arrive_expect_tx(&full, k * R::kSlot);
+      for (int st = 0; st < k; ++st, u &= u - 1u) {
+        const int j = __ffs(u) - 1;
+        if (lane == 0) ptx::bulk_load(s_codes + st * R::kSlot, codes + (size_t)j * R::kSlot, R::kSlot, &full);
+        for (int e = lane * 8; e < R::kExps; e += 256)
+          copy8(ptx::smem_u32(s_exps + st * R::kExps + e), exps + (size_t)j * R::kExps + e);
       }
-      for (int e = lane * 8; e < R::kExps; e += 256)
-        copy8(ptx::smem_u32(s_exps + st * R::kExps + e), exps + (size_t)j * R::kExps + e);
-      arrive_copies(&full[st]);
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&full[st], R::kSlot);
-        ptx::bulk_load(s_codes + st * R::kSlot, codes + (size_t)j * R::kSlot, R::kSlot, &full[st]);
-      }
-      __syncwarp();
+      arrive_copies(&full);
+      if (batch == 0) asm volatile("bar.sync 1, %0;" ::"n"(NT + 32) : "memory");   // the barrier is there for all
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
 
-  const float la = __ldg(p.log_a + bh);
   float* gate = p.s.gate + bh * 2 * nslot;
-  if (tid < p.L) s_lam[tid] = __ldg(p.lam + bh * p.L + tid);
+  if (tid < p.L) s_lam[tid] = lam;
   if (tid < nslot && ((un >> tid) & 1u)) s_w[tid] = expf(gate[par * nslot + tid] + la);
-  const int cc = tid % CPR, r0 = tid / CPR;            // its 16 columns, its first row
-  const Tin* v = static_cast<const Tin*>(p.v) + bh * DV;
-  float qr[R::kRows], kr[R::kRows], qk = 0.f;
+  float qk = 0.f;
 #pragma unroll
-  for (int r = 0; r < R::kRows; ++r) {
-    qr[r] = ld_in(static_cast<const Tin*>(p.q) + bh * DK + r0 + r * (NT / CPR));
-    kr[r] = ld_in(static_cast<const Tin*>(p.k) + bh * DK + r0 + r * (NT / CPR));
+  for (int r = 0; r < R::kRows; ++r)
     if (cc == 0) qk = fmaf(qr[r], kr[r], qk);
-  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, o);
   if (lane == 0) s_qk[warp] = qk;
-  uint64_t carry[R::kRows][8], part[8];
+  uint64_t part[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v0 = ld_in(v + cc * 16 + 2 * i), v1 = ld_in(v + cc * 16 + 2 * i + 1);
-    part[i] = 0ull;
-#pragma unroll
-    for (int r = 0; r < R::kRows; ++r) carry[r][i] = pair(kr[r] * v0, kr[r] * v1);
-  }
-  asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
+  for (int i = 0; i < 8; ++i) part[i] = 0ull;
+  asm volatile("bar.sync 1, %0;" ::"n"(NT + 32) : "memory");
 
-  int i = 0;
+  unsigned u = un;
   bool lost = false;
-  for (unsigned u = un; u != 0u; u &= u - 1u, ++i) {
-    const int j = __ffs(u) - 1, st = i % NS;
-    if (!lost && !ptx::mbar_wait(&full[st], (i / NS) & 1)) {   // reported once; the values are unspecified then
+  const int8_t* my_codes = s_codes + r0 * DV + cc * 16;
+  const uint8_t* my_exps = s_exps + r0 * NB + (cc >> 1);
+  for (int left = cnt, batch = 0; left > 0; left -= NS, ++batch) {
+    const int k = left < NS ? left : NS;
+    if (batch > 0) asm volatile("bar.sync 3, %0;" ::"n"(NT + 32) : "memory");
+    if (!lost && !ptx::mbar_wait(&full, batch & 1)) {   // reported once; the values are unspecified then
       lost = true;
       atomicOr(p.status, LLATTN_DEV_WAIT_TIMEOUT);
     }
-    const float w = s_w[j], lw = w * s_lam[j + 1];
+    for (int st = 0; st < k; ++st, u &= u - 1u) {
+      const int j = __ffs(u) - 1;
+      const float lw = s_w[j] * s_lam[j + 1];
 #pragma unroll
-    for (int r = 0; r < R::kRows; ++r) {
-      const int row = r0 + r * (NT / CPR);
-      const float sc = q8_scale(s_exps[st * R::kExps + row * NB + (cc >> 1)]);
-      uint64_t x[8];
-      pairs16(*reinterpret_cast<const uint4*>(s_codes + st * R::kSlot + row * DV + cc * 16), x);
-      const float f = qr[r] * sc * lw;
-      const uint64_t f2 = pair(f, f);
+      for (int r = 0; r < R::kRows; ++r) {
+        uint64_t x[8];
+        pairs16(*reinterpret_cast<const uint4*>(my_codes + st * R::kSlot + r * (NT / CPR) * DV), x);
+        const float f = qr[r] * q8_scale(my_exps[st * R::kExps + r * (NT / CPR) * NB]) * lw;
+        const uint64_t f2 = pair(f, f);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) part[c] = fma2(f2, x[c], part[c]);
-      if (j < m) {
-        const uint64_t g2 = pair(sc * w, sc * w);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) carry[r][c] = fma2(g2, x[c], carry[r][c]);
+        for (int c = 0; c < 8; ++c) part[c] = fma2(f2, x[c], part[c]);
       }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[st]);
-  }
-
-  if (m < nslot) {
-#pragma unroll
-    for (int r = 0; r < R::kRows; ++r) {
-      const int row = r0 + r * (NT / CPR);
-      const unsigned e = store_codes(carry[r], codes + (size_t)m * R::kSlot + row * DV + cc * 16);
-      if ((cc & 1) == 0) exps[(size_t)m * R::kExps + row * NB + (cc >> 1)] = (uint8_t)e;
     }
   }
 
@@ -396,7 +405,32 @@ __global__ void __launch_bounds__(Ring<DK, DV>::kThreads + 32) q8_step_ring_kern
   }
 #pragma unroll
   for (int q = 0; q < CPR / 2; ++q) s_red[warp][cc * 16 + first + q] = x[q];
-  asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
+
+  // the carry into slot m, with slots 0..m-1 read once more: from their places in the ring, or where
+  // later slots have taken those from the L2 cache.  (Kept through the loop above the carry would
+  // cost a third of the CTAs that fit an SM.)
+  if (m < nslot) {
+    const bool held = cnt <= NS;
+    load16(v + cc * 16, x);
+#pragma unroll
+    for (int r = 0; r < R::kRows; ++r) {
+      const int row = r0 + r * (NT / CPR), at = row * DV + cc * 16, ea = row * NB + (cc >> 1);
+      uint64_t carry[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) carry[c] = pair(kr[r] * x[2 * c], kr[r] * x[2 * c + 1]);
+      for (int j = 0; j < m; ++j) {
+        uint64_t y[8];
+        pairs16(*reinterpret_cast<const uint4*>((held ? s_codes : codes) + (size_t)j * R::kSlot + at), y);
+        const float g = s_w[j] * q8_scale((held ? s_exps : exps)[(size_t)j * R::kExps + ea]);
+        const uint64_t g2 = pair(g, g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) carry[c] = fma2(g2, y[c], carry[c]);
+      }
+      const unsigned e = store_codes(carry, codes + (size_t)m * R::kSlot + at);
+      if ((cc & 1) == 0) exps[(size_t)m * R::kExps + ea] = (uint8_t)e;
+    }
+  }
+  asm volatile("bar.sync 2, %0;" ::"n"(NT) : "memory");
   for (int c = tid; c < DV; c += NT) {
     float s = 0.f, qkt = 0.f;
 #pragma unroll
@@ -475,7 +509,7 @@ cudaError_t launch_step(const Q8StepProblem& p, cudaStream_t st) {
 // value and what the rounding left (off by 2^-17 of itself in all); so do k f and v of fp32 inputs,
 // without the product of the two remainders (2^-16).
 constexpr int kPreTile = 32;       // tokens per stage
-constexpr int kPreStages = 4;
+constexpr int kPreStages = 3;
 constexpr int kPreSeg = 512;       // tokens whose factors are held at a time
 
 // Scratch of a call: piece sums [B, H, pieces, dk, dv], then the log decays of the pieces
@@ -554,28 +588,40 @@ constexpr int pre_smem() {
 template <typename T, int DK, int DV>
 struct Walker;
 
+// Rows of S a warp takes, in sixteens: two where the state has 64 rows, so that every fragment of
+// v that a warp loads serves twice.
+template <typename T, int DK>
+constexpr int kTall = 1;
+
 template <int DK, int DV>
 struct Walker<__nv_bfloat16, DK, DV> {
-  uint32_t ko, vo[DV / 16];
+  static constexpr int MT = kTall<__nv_bfloat16, DK>;
+  uint32_t ko[MT], vo[DV / 16];
   __device__ __forceinline__ Walker(int warp, int lane) {
     const int mi = lane >> 3, r = lane & 7;
-    ko = Tile<__nv_bfloat16, DK>::at(0u, (mi >> 1) * 8 + r, 2 * warp + (mi & 1));
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      ko[i] = Tile<__nv_bfloat16, DK>::at(0u, (mi >> 1) * 8 + r, 2 * (MT * warp + i) + (mi & 1));
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n) vo[n] = Tile<__nv_bfloat16, DV>::at(0u, (mi & 1) * 8 + r, 2 * n + (mi >> 1));
   }
-  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
+  __device__ __forceinline__ void step(float (&acc)[MT][DV / 8][4], uint32_t ks, uint32_t vs, int t0,
                                        const float (&f)[4]) const {
-    unsigned raw[4], big[4], rest[4], b[DV / 16][4];
-    ldmatrix4t(raw, ks + t0 * (DK * 2) + ko);
+    unsigned raw[MT][4], big[4], rest[4], b[DV / 16][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ldmatrix4t(raw[i], ks + t0 * (DK * 2) + ko[i]);
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n) ldmatrix4t(b[n], vs + t0 * (DV * 2) + vo[n]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      split2(bf16_lo(raw[i]) * f[i & 2], bf16_hi(raw[i]) * f[(i & 2) + 1], big[i], rest[i]);
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-    for (int n = 0; n < DV / 8; ++n) mma_bf16(acc[n], big, b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+      for (int i = 0; i < 4; ++i)
+        split2(bf16_lo(raw[mt][i]) * f[i & 2], bf16_hi(raw[mt][i]) * f[(i & 2) + 1], big[i], rest[i]);
 #pragma unroll
-    for (int n = 0; n < DV / 8; ++n) mma_bf16(acc[n], rest, b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+      for (int n = 0; n < DV / 8; ++n) mma_bf16(acc[mt][n], big, b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+#pragma unroll
+      for (int n = 0; n < DV / 8; ++n) mma_bf16(acc[mt][n], rest, b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+    }
   }
 };
 
@@ -583,8 +629,9 @@ template <int DK, int DV>
 struct Walker<float, DK, DV> {
   int row, tok;
   __device__ __forceinline__ Walker(int warp, int lane) : row(16 * warp + (lane >> 2)), tok(2 * (lane & 3)) {}
-  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
+  __device__ __forceinline__ void step(float (&sums)[1][DV / 8][4], uint32_t ks, uint32_t vs, int t0,
                                        const float (&f)[4]) const {
+    float (&acc)[DV / 8][4] = sums[0];
     using K = Tile<float, DK>;
     using V = Tile<float, DV>;
     const int t = t0 + tok, g = row & 7;   // (the fragment's column has the lane's row within 8)
@@ -641,8 +688,8 @@ struct Copier {
 
 // Grid: (head, piece or short level, sequence), heads first: adjacent CTAs read adjacent rows.
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, PreScratch ws) {
-  constexpr int NT = 2 * DK, NB = DV / 32;
+__global__ void __launch_bounds__(2 * DK / kTall<T, DK>) q8_prefill_kernel(Q8PrefillProblem p, PreScratch ws) {
+  constexpr int MT = kTall<T, DK>, NT = 2 * DK / MT, NB = DV / 32;
   using K = Tile<T, DK>;
   using V = Tile<T, DV>;
   extern __shared__ float4 pre_smem_raw[];
@@ -674,11 +721,13 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
   const T* k = static_cast<const T*>(p.k) + ((size_t)sp.start * p.H + h) * DK;
   const T* v = static_cast<const T*>(p.v) + ((size_t)sp.start * p.H + h) * DV;
   const float* la = p.log_a + (size_t)sp.start * p.H + h;
-  float acc[DV / 8][4];
+  float acc[MT][DV / 8][4];
 #pragma unroll
-  for (int i = 0; i < DV / 8; ++i)
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int i = 0; i < DV / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[mt][i][j] = 0.f;
   const Walker<T, DK, DV> walk(warp, lane);
   const Copier<T, DK, NT> kcopy(k, (size_t)p.H * DK, tid);
   const Copier<T, DV, NT> vcopy(v, (size_t)p.H * DV, tid);
@@ -740,15 +789,19 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
     }
   }
 
+  ptx::griddep_launch_dependents();       // the join's CTAs may come as these leave
   const size_t bh = (size_t)b * p.H + h;
-  const int row = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
+  const int row = 16 * MT * warp + (lane >> 2), c0 = 2 * (lane & 3);
   if (piece) {
     float* out = ws.sum + (bh * ws.pieces + blockIdx.y) * (DK * DV);
 #pragma unroll
-    for (int i = 0; i < DV / 8; ++i) {
-      *reinterpret_cast<float2*>(out + row * DV + 8 * i + c0) = make_float2(acc[i][0], acc[i][1]);
-      *reinterpret_cast<float2*>(out + (row + 8) * DV + 8 * i + c0) = make_float2(acc[i][2], acc[i][3]);
-    }
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < DV / 8; ++i) {
+        float* o = out + (row + 16 * mt) * DV + 8 * i + c0;
+        *reinterpret_cast<float2*>(o) = make_float2(acc[mt][i][0], acc[mt][i][1]);
+        *reinterpret_cast<float2*>(o + 8 * DV) = make_float2(acc[mt][i][2], acc[mt][i][3]);
+      }
     if (tid == 0) ws.piece_log[bh * ws.pieces + blockIdx.y] = D;
     return;
   }
@@ -757,13 +810,14 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
 #pragma unroll
   for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {   // rows g and g + 8
+    for (int half = 0; half < 2 * MT; ++half) {   // rows g, g + 8, and those of the second sixteen
+      const int mt = half >> 1, pick = 2 * (half & 1);
       unsigned top = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          top = max(top, __float_as_uint(acc[4 * blk + i][2 * half + j]) & 0x7fffffffu);
+          top = max(top, __float_as_uint(acc[mt][4 * blk + i][pick + j]) & 0x7fffffffu);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const unsigned e = q8_exp(top);
@@ -772,7 +826,7 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
       int8_t* codes = p.s.codes + (at * DK + rr) * DV + 32 * blk + c0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int x0 = q8_code(acc[4 * blk + i][2 * half], inv, e), x1 = q8_code(acc[4 * blk + i][2 * half + 1], inv, e);
+        const int x0 = q8_code(acc[mt][4 * blk + i][pick], inv, e), x1 = q8_code(acc[mt][4 * blk + i][pick + 1], inv, e);
         *reinterpret_cast<uint16_t*>(codes + 8 * i) = (uint16_t)((x0 & 0xff) | ((x1 & 0xff) << 8));
       }
       if ((lane & 3) == 0) p.s.exps[(at * DK + rr) * NB + blk] = (uint8_t)e;
@@ -785,6 +839,7 @@ constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(Q8PrefillProblem p, PreScratch ws, int parts) {
   __shared__ float s_w[kJoinThreads], s_lvl[32];
+  ptx::griddep_wait();                    // the pieces are summed and visible
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, nslot = p.L - 1;
   const SeqSpan sp = seq_span(b, p.T, p.cu_seqlens, p.status);
   const int n = sp.len;
@@ -870,14 +925,14 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(Q8PrefillProblem 
   if ((tid & 7) == 0) p.s.exps[at / kQ8Block] = (uint8_t)e;
 }
 
-// Tokens of a piece: 512, an eighth of whose bytes its sums are; more where the pieces of a call
-// would be over 4096 of 64 x 64 values (64 MB of sums), fewer, 128 at least, where they would leave
-// the machine half empty.
+// Tokens of a piece: 512 (its sums are an eighth of its bytes), more while the pieces of a call
+// stay 2048 at least and until they are 4096 of 64 x 64 values at most (64 MB of sums), fewer, 128 at
+// least, where they would leave the machine half empty.
 int piece_log2(int B, int H, int T, int dk, int dv) {
   const long long bh = (long long)B * H;
   int j = 9;
   while (j > 7 && bh * (T >> j) < 4 * 148) --j;
-  while (j < 24 && bh * (T >> j) * dk * dv > 4096ll * 64 * 64) ++j;
+  while (j < 24 && (bh * (T >> (j + 1)) >= 2048 || bh * (T >> j) * dk * dv > 4096ll * 64 * 64)) ++j;
   return j;
 }
 
@@ -906,7 +961,8 @@ cudaError_t launch_prefill_one(const Q8PrefillProblem& p, const PreScratch& s, c
     if (e != cudaSuccess) return e;
     allowed[dev].store(true);
   }
-  q8_prefill_kernel<T, DK, DV><<<dim3(p.H, s.pieces + s.shorts, p.B), 2 * DK, smem, st>>>(p, s);
+  q8_prefill_kernel<T, DK, DV>
+      <<<dim3(p.H, s.pieces + s.shorts, p.B), 2 * DK / kTall<T, DK>, smem, st>>>(p, s);
   return cudaGetLastError();
 }
 
@@ -945,45 +1001,49 @@ __device__ __forceinline__ void store16(__nv_bfloat16* o, const float (&x)[16]) 
   *reinterpret_cast<uint4*>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-constexpr int kReadEach = 4;       // pieces of a thread, asked for together
+constexpr int kReadEach = 4;       // slots of a thread, asked for together: the same piece of each
 
+// Grid: (256 pieces of a slot, kReadEach slots of the output).
 template <typename Tout>
-__global__ void __launch_bounds__(256) q8_read_kernel(Q8ReadProblem p, long long total) {
-  // total = 16-value pieces of the output; per: pieces of one (sequence, head) slot
-  const int per = p.dk * p.dv / 16, nslot = p.L - 1;
-  const long long i0 = (long long)blockIdx.x * (256 * kReadEach) + threadIdx.x;
+__global__ void __launch_bounds__(256) q8_read_kernel(Q8ReadProblem p, long long slots) {
+  const int per = p.dk * p.dv / 16, nslot = p.L - 1, piece = blockIdx.x * 256 + threadIdx.x;
+  if (piece >= per) return;
+  const long long s0 = ((long long)blockIdx.z * gridDim.y + blockIdx.y) * kReadEach;
   uint4 u[kReadEach];
   unsigned e[kReadEach];
-  long long to[kReadEach];
+  bool there[kReadEach];
 #pragma unroll
   for (int r = 0; r < kReadEach; ++r) {
-    const long long i = i0 + r * 256;
-    to[r] = -1;
-    if (i >= total) continue;
-    const long long s = i / per;
-    const int piece = (int)(i - s * per);
+    const long long s = s0 + r;
+    there[r] = s < slots;
+    if (!there[r]) continue;
     long long src = s;
     if (p.slot) {
-      const int j = __ldg(p.slot + (int)(s / p.H));
+      const int j = __ldg(p.slot + (int)((unsigned)s / (unsigned)p.H));   // (s < B * H < 2^32 here)
       if (j < 0 || j >= nslot) {
-        atomicOr(p.status, LLATTN_DEV_DECODE_POS);
+        there[r] = false;
+        if (piece == 0) atomicOr(p.status, LLATTN_DEV_DECODE_POS);
         continue;
       }
       src = s * nslot + j;
     }
     u[r] = __ldcs(reinterpret_cast<const uint4*>(p.s.codes + src * p.dk * p.dv) + piece);
     e[r] = p.s.exps[src * (p.dk * p.dv / 32) + (piece >> 1)];
-    to[r] = i * 16;
   }
 #pragma unroll
   for (int r = 0; r < kReadEach; ++r) {
-    if (to[r] < 0) continue;
+    if (!there[r]) continue;
+    uint64_t y[8];
     float x[16];
-    unpack16(u[r], x);
+    pairs16(u[r], y);
     const float sc = q8_scale(e[r]);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) x[c] *= sc;
-    store16(static_cast<Tout*>(p.out) + to[r], x);
+    for (int c = 0; c < 8; ++c) {
+      unpair(y[c], x[2 * c], x[2 * c + 1]);
+      x[2 * c] *= sc;
+      x[2 * c + 1] *= sc;
+    }
+    store16(static_cast<Tout*>(p.out) + (s0 + r) * p.dk * p.dv + piece * 16, x);
   }
 }
 
@@ -1009,19 +1069,28 @@ cudaError_t q8_prefill(const Q8PrefillProblem& p, void* ws, cudaStream_t st) {
                                                   : launch_prefill<float>(p, s, st);
   if (e != cudaSuccess) return e;
   const int longs = s.pieces ? p.L - 1 - (s.ch_log + 1) : 0, parts = p.dk * p.dv / 1024;
-  q8_join_kernel<<<dim3(1 + (longs > 0 ? longs * parts : 0), p.H, p.B), kJoinThreads, 0, st>>>(p, s, parts);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1 + (longs > 0 ? longs * parts : 0), p.H, p.B);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, q8_join_kernel, p, s, parts);
 }
 
 cudaError_t q8_read(const Q8ReadProblem& p, cudaStream_t st) {
+  if (p.L < 2) return cudaSuccess;
   const long long slots = (long long)p.B * p.H * (p.slot ? 1 : p.L - 1);
-  const long long total = slots * (p.dk * p.dv / 16);
-  if (total == 0 || p.L < 2) return cudaSuccess;
-  const long long each = 256 * kReadEach, grid = (total + each - 1) / each;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const long long groups = (slots + kReadEach - 1) / kReadEach;
+  const unsigned y = (unsigned)(groups < 32768 ? groups : 32768), z = (unsigned)((groups + y - 1) / y);
+  if (z > 65535u) return cudaErrorInvalidConfiguration;
+  const dim3 grid((p.dk * p.dv / 16 + 255) / 256, y, z);
   count_launch();
-  if (p.out_dtype == LLATTN_BF16) q8_read_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(p, total);
-  else q8_read_kernel<float><<<(unsigned)grid, 256, 0, st>>>(p, total);
+  if (p.out_dtype == LLATTN_BF16) q8_read_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p, slots);
+  else q8_read_kernel<float><<<grid, 256, 0, st>>>(p, slots);
   return cudaGetLastError();
 }
 

@@ -69,7 +69,8 @@ def test_qk_empty_calls_and_workspace():
     assert _call("llattn_qk_norm_rope", QK_ORDER, QK, dict(N=0, q=None, qo=None, pos=None)) == OK
     assert _call("llattn_qk_norm_rope_bwd", QKB_ORDER, QKB, dict(N=0, dwq=None, dwk=None)) == OK
     assert binding.qk_norm_rope_bwd_workspace_bytes(64, False) == 0
-    assert binding.qk_norm_rope_bwd_workspace_bytes(64, True) > 0
+    for d in (32, 64, 128):          # what the binding allocates without asking
+        assert binding.qk_norm_rope_bwd_workspace_bytes(d, True) == 148 * 2 * 2 * d * 4
     with pytest.raises(binding.LLAttnError):
         binding.qk_norm_rope_bwd_workspace_bytes(48)
 
