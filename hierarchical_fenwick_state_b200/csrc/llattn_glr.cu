@@ -164,6 +164,9 @@ struct Job {
   long long start;
 };
 
+// The CTA's next tile: time tile by time tile, so that it comes after all that it looks back at.  By
+// the counter `next`, or where there is none by turns (the grid's CTAs are then all resident, or no
+// tile looks back).
 template <int TT>
 __device__ __forceinline__ Job take_job(unsigned* next, unsigned& turn, unsigned total, int nseq,
                                         int cts, int T, const int* cu, unsigned int* status) {
@@ -172,7 +175,7 @@ __device__ __forceinline__ Job take_job(unsigned* next, unsigned& turn, unsigned
     unsigned i;
     if (next) {
       i = atomicAdd(next, 1u);
-    } else {   // one tile in time for each sequence: no order to keep
+    } else {
       i = turn;
       turn += gridDim.x;
     }
@@ -534,53 +537,79 @@ __global__ void __launch_bounds__(kWalkThreads) glr_bwd_walk(GlrBwdProblem p) {
 constexpr int kWalkT = 16;   // a tile's threads have a step each at best below it
 
 constexpr int kTileSteps = 64;   // the fewest steps a tile has, which sizes the scratch
-constexpr int kSms = 148;
+// Sequences times channel tiles up to which tiles are handed out by turns.  A chain of tiles moves
+// at the pace of its slowest, and turns keep neighbours in time in step: one sequence of 65536 x
+// 1024 takes 250 us backward by turns and 340 by the counter, 65536 x 2048 479 and 573.  Many
+// chains hide that, and the counter evens out the SMs: 8 x 9600 x 1024 takes 273 us by the counter
+// and 291 by turns, 32 x 2048 x 1024 240 and 263.
+constexpr int kFewChains = 128;
 
 size_t scratch_bytes(int nseq, int T, int D, int tt) {
   return kScratchHead + (size_t)((T + tt - 1) / tt) * nseq * ((D + kCT - 1) / kCT) * kCT * sizeof(Record);
 }
 
-// The dynamic shared-memory opt-in is a per-device attribute of each kernel: asked for once.
-using Allowed = std::atomic<bool>[64];
+// What a kernel is asked for once on each device: its shared memory (an opt-in there), and how many
+// of its CTAs the device holds.
+using Resident = std::atomic<int>[64];
 
 template <typename Kernel>
-cudaError_t allow_smem(Kernel kernel, Allowed& allowed, size_t smem) {
-  int dev = 0;
+cudaError_t resident_ctas(Kernel kernel, Resident& held, int threads, size_t smem, int* ctas) {
+  int dev = 0, each = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (allowed[dev].load()) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) allowed[dev].store(true);
-  return e;
+  if ((*ctas = held[dev].load()) > 0) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
+      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, threads, smem)) != cudaSuccess ||
+      (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return e;
+  if ((*ctas = each * sms) < 1) return cudaErrorInvalidConfiguration;
+  held[dev].store(*ctas);
+  return cudaSuccess;
 }
 
 template <typename Problem>
-cudaError_t launch_tiles(void (*kernel)(Problem, Scratch, int, unsigned), Allowed& allowed,
-                         const Problem& p, int tt, int threads, int ctas_per_sm, size_t smem,
-                         void* ws, cudaStream_t st) {
+cudaError_t launch_tiles(void (*kernel)(Problem, Scratch, int, unsigned), Resident& held,
+                         const Problem& p, int tt, int threads, size_t smem, void* ws,
+                         cudaStream_t st) {
   const int cts = (p.D + kCT - 1) / kCT, tiles = (p.T + tt - 1) / tt;
   Scratch s{static_cast<unsigned*>(ws),
             reinterpret_cast<Record*>(static_cast<char*>(ws) + kScratchHead)};
-  const unsigned total = (unsigned)tiles * p.nseq * cts, most = kSms * ctas_per_sm;
-  cudaError_t e = allow_smem(kernel, allowed, smem);
+  const unsigned total = (unsigned)tiles * p.nseq * cts;
+  int most = 0;
+  cudaError_t e = resident_ctas(kernel, held, threads, smem, &most);
   if (e != cudaSuccess) return e;
-  if (tiles == 1) s = {nullptr, nullptr};
-  else if ((e = cudaMemsetAsync(ws, 0, scratch_bytes(p.nseq, p.T, p.D, tt), st)) != cudaSuccess) return e;
-  kernel<<<total < most ? total : most, threads, smem, st>>>(p, s, cts, total);
+  if (tiles > 1 && (e = cudaMemsetAsync(ws, 0, scratch_bytes(p.nseq, p.T, p.D, tt), st)) != cudaSuccess) return e;
+  const unsigned grid = total < (unsigned)most ? total : (unsigned)most;
+  if (tiles == 1 || p.nseq * (long long)cts <= kFewChains) {
+    Scratch turns = s;
+    turns.next = nullptr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;   // every CTA is resident: a tile looked back at is in hand
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = tiles == 1 ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, turns, cts, total);
+  }
+  kernel<<<grid, threads, smem, st>>>(p, s, cts, total);
   return cudaGetLastError();
 }
 
 template <typename T, int NT, int VEC, int S, int MINB>
 cudaError_t fwd_tiles(const GlrProblem& p, void* ws, cudaStream_t st) {
-  static Allowed allowed;
-  return launch_tiles(glr_fwd_tiles<T, NT, VEC, S, MINB>, allowed, p, NT * VEC / kCT * S, NT, MINB,
+  static Resident held;
+  return launch_tiles(glr_fwd_tiles<T, NT, VEC, S, MINB>, held, p, NT * VEC / kCT * S, NT,
                       sizeof(FwdShared<T, NT, VEC, S>), ws, st);
 }
 template <int NT, int VEC, int S, int MINB>
 cudaError_t bwd_tiles(const GlrBwdProblem& p, void* ws, cudaStream_t st) {
-  static Allowed allowed;
-  return launch_tiles(glr_bwd_tiles<NT, VEC, S, MINB>, allowed, p, NT * VEC / kCT * S, NT, MINB,
+  static Resident held;
+  return launch_tiles(glr_bwd_tiles<NT, VEC, S, MINB>, held, p, NT * VEC / kCT * S, NT,
                       sizeof(BwdShared<NT, VEC, S>), ws, st);
 }
 
