@@ -505,9 +505,9 @@ cudaError_t launch_step(const Q8StepProblem& p, cudaStream_t st) {
 //
 // Arithmetic.  The products run on the tensor cores as mma.sync of bf16 with fp32 sums: the kernel
 // is bound by reading k and v once (512 bytes of fp32 or 256 of bf16 per 8192 operations at d = 64),
-// and a warp's 16 rows of S fit its registers.  f k is not a bf16: it goes in as two, the rounded
-// value and what the rounding left (off by 2^-17 of itself in all); so do k f and v of fp32 inputs,
-// without the product of the two remainders (2^-16).
+// and a warp's 16 rows of S fit its registers.  f k is not a bf16: it goes in as three, the rounded
+// value and twice what the rounding left, which is all of fp32's bits; of fp32 inputs v does too, and
+// the three smallest of the nine products (2^-24 of the whole and less) are left out.
 constexpr int kPreTile = 32;       // tokens per stage
 constexpr int kPreStages = 3;
 constexpr int kPreSeg = 512;       // tokens whose factors are held at a time
@@ -528,16 +528,21 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(unsigned w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(unsigned w) { return __uint_as_float(w & 0xffff0000u); }
 
-// (x, y) as a rounded pair and the pair of what the rounding left.
-__device__ __forceinline__ void split2(float x, float y, unsigned& big, unsigned& rest) {
-  big = pack_bf16(x, y);
-  rest = pack_bf16(x - bf16_lo(big), y - bf16_hi(big));
+// (x, y) as three pairs: rounded, what the rounding left, rounded, and what that left (exact but for
+// fp32's last bits).
+__device__ __forceinline__ void split3(float x, float y, unsigned (&part)[3]) {
+  part[0] = pack_bf16(x, y);
+  x -= bf16_lo(part[0]);
+  y -= bf16_hi(part[0]);
+  part[1] = pack_bf16(x, y);
+  part[2] = pack_bf16(x - bf16_lo(part[1]), y - bf16_hi(part[1]));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
+__device__ __forceinline__ void mma_bf16(float (&c)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3,
+                                         unsigned b0, unsigned b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void ldmatrix4t(unsigned (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -588,40 +593,28 @@ constexpr int pre_smem() {
 template <typename T, int DK, int DV>
 struct Walker;
 
-// Rows of S a warp takes, in sixteens: two where the state has 64 rows, so that every fragment of
-// v that a warp loads serves twice.
-template <typename T, int DK>
-constexpr int kTall = 1;
-
 template <int DK, int DV>
 struct Walker<__nv_bfloat16, DK, DV> {
-  static constexpr int MT = kTall<__nv_bfloat16, DK>;
-  uint32_t ko[MT], vo[DV / 16];
+  uint32_t ko, vo[DV / 16];
   __device__ __forceinline__ Walker(int warp, int lane) {
     const int mi = lane >> 3, r = lane & 7;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      ko[i] = Tile<__nv_bfloat16, DK>::at(0u, (mi >> 1) * 8 + r, 2 * (MT * warp + i) + (mi & 1));
+    ko = Tile<__nv_bfloat16, DK>::at(0u, (mi >> 1) * 8 + r, 2 * warp + (mi & 1));
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n) vo[n] = Tile<__nv_bfloat16, DV>::at(0u, (mi & 1) * 8 + r, 2 * n + (mi >> 1));
   }
-  __device__ __forceinline__ void step(float (&acc)[MT][DV / 8][4], uint32_t ks, uint32_t vs, int t0,
+  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
                                        const float (&f)[4]) const {
-    unsigned raw[MT][4], big[4], rest[4], b[DV / 16][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) ldmatrix4t(raw[i], ks + t0 * (DK * 2) + ko[i]);
+    unsigned raw[4], kf[4][3], b[DV / 16][4];
+    ldmatrix4t(raw, ks + t0 * (DK * 2) + ko);
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n) ldmatrix4t(b[n], vs + t0 * (DV * 2) + vo[n]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int i = 0; i < 4; ++i) split3(bf16_lo(raw[i]) * f[i & 2], bf16_hi(raw[i]) * f[(i & 2) + 1], kf[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        split2(bf16_lo(raw[mt][i]) * f[i & 2], bf16_hi(raw[mt][i]) * f[(i & 2) + 1], big[i], rest[i]);
+    for (int q = 0; q < 3; ++q)
 #pragma unroll
-      for (int n = 0; n < DV / 8; ++n) mma_bf16(acc[mt][n], big, b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
-#pragma unroll
-      for (int n = 0; n < DV / 8; ++n) mma_bf16(acc[mt][n], rest, b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
-    }
+      for (int n = 0; n < DV / 8; ++n)
+        mma_bf16(acc[n], kf[0][q], kf[1][q], kf[2][q], kf[3][q], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
   }
 };
 
@@ -629,32 +622,32 @@ template <int DK, int DV>
 struct Walker<float, DK, DV> {
   int row, tok;
   __device__ __forceinline__ Walker(int warp, int lane) : row(16 * warp + (lane >> 2)), tok(2 * (lane & 3)) {}
-  __device__ __forceinline__ void step(float (&sums)[1][DV / 8][4], uint32_t ks, uint32_t vs, int t0,
+  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
                                        const float (&f)[4]) const {
-    float (&acc)[DV / 8][4] = sums[0];
     using K = Tile<float, DK>;
     using V = Tile<float, DV>;
     const int t = t0 + tok, g = row & 7;   // (the fragment's column has the lane's row within 8)
-    unsigned big[4], rest[4];
+    unsigned kf[4][3];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int tt = t + (i >> 1) * 8, rr = row + (i & 1) * 8;
-      split2(K::get(ks, tt, rr) * f[i & 2], K::get(ks, tt + 1, rr) * f[(i & 2) + 1], big[i], rest[i]);
+      split3(K::get(ks, tt, rr) * f[i & 2], K::get(ks, tt + 1, rr) * f[(i & 2) + 1], kf[i]);
     }
 #pragma unroll
     for (int n0 = 0; n0 < DV / 8; n0 += 4) {
-      unsigned vb[4][2], vr[4][2];
+      unsigned vp[4][2][3];
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          split2(V::get(vs, t + 8 * i, 8 * (n0 + n) + g), V::get(vs, t + 8 * i + 1, 8 * (n0 + n) + g), vb[n][i], vr[n][i]);
+          split3(V::get(vs, t + 8 * i, 8 * (n0 + n) + g), V::get(vs, t + 8 * i + 1, 8 * (n0 + n) + g), vp[n][i]);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) mma_bf16(acc[n0 + n], big, vb[n][0], vb[n][1]);
+      for (int q = 0; q < 3; ++q)
 #pragma unroll
-      for (int n = 0; n < 4; ++n) mma_bf16(acc[n0 + n], rest, vb[n][0], vb[n][1]);
+        for (int w = 0; w < 3 - q; ++w)
 #pragma unroll
-      for (int n = 0; n < 4; ++n) mma_bf16(acc[n0 + n], big, vr[n][0], vr[n][1]);
+          for (int n = 0; n < 4; ++n)
+            mma_bf16(acc[n0 + n], kf[0][q], kf[1][q], kf[2][q], kf[3][q], vp[n][0][w], vp[n][1][w]);
     }
   }
 };
@@ -688,8 +681,8 @@ struct Copier {
 
 // Grid: (head, piece or short level, sequence), heads first: adjacent CTAs read adjacent rows.
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(2 * DK / kTall<T, DK>) q8_prefill_kernel(Q8PrefillProblem p, PreScratch ws) {
-  constexpr int MT = kTall<T, DK>, NT = 2 * DK / MT, NB = DV / 32;
+__global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, PreScratch ws) {
+  constexpr int NT = 2 * DK, NB = DV / 32;
   using K = Tile<T, DK>;
   using V = Tile<T, DV>;
   extern __shared__ float4 pre_smem_raw[];
@@ -721,13 +714,11 @@ __global__ void __launch_bounds__(2 * DK / kTall<T, DK>) q8_prefill_kernel(Q8Pre
   const T* k = static_cast<const T*>(p.k) + ((size_t)sp.start * p.H + h) * DK;
   const T* v = static_cast<const T*>(p.v) + ((size_t)sp.start * p.H + h) * DV;
   const float* la = p.log_a + (size_t)sp.start * p.H + h;
-  float acc[MT][DV / 8][4];
+  float acc[DV / 8][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int i = 0; i < DV / 8; ++i)
 #pragma unroll
-    for (int i = 0; i < DV / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[mt][i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
   const Walker<T, DK, DV> walk(warp, lane);
   const Copier<T, DK, NT> kcopy(k, (size_t)p.H * DK, tid);
   const Copier<T, DV, NT> vcopy(v, (size_t)p.H * DV, tid);
@@ -791,17 +782,15 @@ __global__ void __launch_bounds__(2 * DK / kTall<T, DK>) q8_prefill_kernel(Q8Pre
 
   ptx::griddep_launch_dependents();       // the join's CTAs may come as these leave
   const size_t bh = (size_t)b * p.H + h;
-  const int row = 16 * MT * warp + (lane >> 2), c0 = 2 * (lane & 3);
+  const int row = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
   if (piece) {
     float* out = ws.sum + (bh * ws.pieces + blockIdx.y) * (DK * DV);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i = 0; i < DV / 8; ++i) {
-        float* o = out + (row + 16 * mt) * DV + 8 * i + c0;
-        *reinterpret_cast<float2*>(o) = make_float2(acc[mt][i][0], acc[mt][i][1]);
-        *reinterpret_cast<float2*>(o + 8 * DV) = make_float2(acc[mt][i][2], acc[mt][i][3]);
-      }
+    for (int i = 0; i < DV / 8; ++i) {
+      float* o = out + row * DV + 8 * i + c0;
+      *reinterpret_cast<float2*>(o) = make_float2(acc[i][0], acc[i][1]);
+      *reinterpret_cast<float2*>(o + 8 * DV) = make_float2(acc[i][2], acc[i][3]);
+    }
     if (tid == 0) ws.piece_log[bh * ws.pieces + blockIdx.y] = D;
     return;
   }
@@ -810,14 +799,13 @@ __global__ void __launch_bounds__(2 * DK / kTall<T, DK>) q8_prefill_kernel(Q8Pre
 #pragma unroll
   for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-    for (int half = 0; half < 2 * MT; ++half) {   // rows g, g + 8, and those of the second sixteen
-      const int mt = half >> 1, pick = 2 * (half & 1);
+    for (int half = 0; half < 2; ++half) {   // rows g and g + 8
       unsigned top = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          top = max(top, __float_as_uint(acc[mt][4 * blk + i][pick + j]) & 0x7fffffffu);
+          top = max(top, __float_as_uint(acc[4 * blk + i][2 * half + j]) & 0x7fffffffu);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const unsigned e = q8_exp(top);
@@ -826,7 +814,7 @@ __global__ void __launch_bounds__(2 * DK / kTall<T, DK>) q8_prefill_kernel(Q8Pre
       int8_t* codes = p.s.codes + (at * DK + rr) * DV + 32 * blk + c0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int x0 = q8_code(acc[mt][4 * blk + i][pick], inv, e), x1 = q8_code(acc[mt][4 * blk + i][pick + 1], inv, e);
+        const int x0 = q8_code(acc[4 * blk + i][2 * half], inv, e), x1 = q8_code(acc[4 * blk + i][2 * half + 1], inv, e);
         *reinterpret_cast<uint16_t*>(codes + 8 * i) = (uint16_t)((x0 & 0xff) | ((x1 & 0xff) << 8));
       }
       if ((lane & 3) == 0) p.s.exps[(at * DK + rr) * NB + blk] = (uint8_t)e;
@@ -961,8 +949,7 @@ cudaError_t launch_prefill_one(const Q8PrefillProblem& p, const PreScratch& s, c
     if (e != cudaSuccess) return e;
     allowed[dev].store(true);
   }
-  q8_prefill_kernel<T, DK, DV>
-      <<<dim3(p.H, s.pieces + s.shorts, p.B), 2 * DK / kTall<T, DK>, smem, st>>>(p, s);
+  q8_prefill_kernel<T, DK, DV><<<dim3(p.H, s.pieces + s.shorts, p.B), 2 * DK, smem, st>>>(p, s);
   return cudaGetLastError();
 }
 
