@@ -31,7 +31,6 @@ namespace llattn {
 namespace {
 
 constexpr int kQkThreads = 256;
-constexpr int kQkWarps = kQkThreads / 32;
 constexpr int kQkTable = 2048;     // (cosine, sine) pairs of a batch at most
 constexpr int kSms = 148;
 

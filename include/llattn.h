@@ -467,7 +467,8 @@ LLATTN_API llattn_status llattn_gdn_fwd(int in_dtype, const void* q, const void*
  *              Gk, all at most 65535; eps > 0 and finite; strides at least G*d.
  * Pointers q, k, qo, ko 16-byte aligned and strides a multiple of 16 bytes, the rest 4-byte
  * aligned; no output may overlap an input or the other output.  No scratch memory.
- * Asynchronous on `stream`.  A row that holds an infinity or NaN gives NaN in that row alone.
+ * Asynchronous on `stream`.  A row that holds an infinity or NaN gives NaN in that row alone; a row
+ * whose sum of squares leaves fp32's range (values around 1e19) gives zeros.
  */
 enum { LLATTN_NORM_L2 = 0, LLATTN_NORM_RMS = 1 };
 enum { LLATTN_ROPE_HALF = 0, LLATTN_ROPE_INTERLEAVED = 1 };

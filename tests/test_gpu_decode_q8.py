@@ -6,7 +6,7 @@ Reference: the definition in 64 bits on the CPU, from the held codes.  Bounds (u
     terms' absolute values;
   * a carried value differs from the exact one by 128 u of the same kind of sum, and is then rounded
     by half a step of its block's power of two;
-  * a prompt's sum: operands split into two bf16 parts (off by 2^-16), products and sums over a
+  * a prompt's sum: operands split into bf16 parts (off by 2^-16 at most), products and sums over a
     bucket in fp32, decays from log sums below 32 (about 2^-15): 2^-13 of the sum of the terms'
     absolute values, then half a step;
   * a block's power of two is the smallest that holds it: checked on its exact largest value, but
@@ -235,6 +235,9 @@ def _prompt_levels(k, v, la, s, n, lvl):
     ([517], 1, 12, 32, 128, "f32", "strong", False), ([2047, 1], 2, 12, 128, 32, "bf16", "zero", True),
     ([4100, 97], 1, 17, 64, 128, "bf16", "slow", True), ([64, 64, 64], 5, 8, 32, 32, "bf16", "strong", False),
     ([9000], 2, 15, 64, 64, "bf16", "slow", False),
+    ([66000], 1, 18, 32, 32, "bf16", "slow", False),        # a bucket of 512 pieces
+    ([2048, 1500, 2047, 512], 64, 13, 32, 32, "bf16", "slow", True),   # pieces of 512
+    ([5000, 4096], 1, 14, 64, 64, "f32", "slow", True),
 ])
 def test_prompt(lengths, H, L, dk, dv, dtype, gates, packed):
     k, v, la, cu, dev = _prompt(lengths, H, dk, dv, dtype, gates, packed)
@@ -406,6 +409,27 @@ def test_other_stream_and_graph_replay():
             c.copy_(x[t])
         graph.replay()
         assert torch.equal(out, want[t]), t
+
+
+def test_the_librarys_buffer_and_a_callers_workspace():
+    """llattn_prefill_state_q8 without a workspace and with one full of noise: the same bytes."""
+    k, v, la, cu, dev = _prompt([3000, 1111], 4, 64, 64, "bf16", "slow", True)
+    B, H, T, L, d = 2, 4, 3000, 13, 64
+    want, _ = _buffer(B, H, L, d, d)
+    blank = want.clone()
+    c = cu.to(DEV)
+    binding.prefill_state_q8(*dev, want, B, H, T, L, d, d, cu_seqlens=c)
+    n = binding.prefill_q8_workspace_bytes(B, H, T, L, d, d)
+    noise = torch.randint(0, 256, (n,), device=DEV).to(torch.uint8)
+    s = torch.cuda.current_stream().cuda_stream
+    args = [binding.BF16] + [t.data_ptr() for t in dev]
+    for ws, size in ((None, 0), (noise.data_ptr(), n)):
+        state = blank.clone()
+        assert binding.lib().llattn_prefill_state_q8(*args, state.data_ptr(), B, H, T, L, d, d, c.data_ptr(), ws, size,
+                                                     s) == 0
+        assert torch.equal(state, want)
+    assert binding.lib().llattn_prefill_state_q8(*args, want.data_ptr(), B, H, T, L, d, d, c.data_ptr(), noise.data_ptr(),
+                                                 n - 1, s) == 7
 
 
 def test_no_levels():

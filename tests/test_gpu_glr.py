@@ -181,7 +181,8 @@ def test_gradients_against_differences():
         assert abs((f[0] - f[1]) / 2e-4 - (dev * d).sum()) <= 2e-5 * (dev * d).abs().sum()
 
 
-@pytest.mark.parametrize("B,T,D", [(1, 65536, 64), (3, 9000, 1000), (1, 30000, 6), (160, 50, 260)])
+@pytest.mark.parametrize("B,T,D", [(1, 65536, 64), (3, 9000, 1000), (1, 30000, 6), (160, 50, 260), (40, 1500, 132),
+                                   (50, 1100, 131), (2, 4000, 4099)])
 def test_long_and_wide(B, T, D):
     """Split walks over long sequences, sampled channels against the recurrence in 64 bits."""
     g = torch.Generator(device=DEV).manual_seed(T)
@@ -200,6 +201,72 @@ def test_long_and_wide(B, T, D):
     dx, dla, _, E, Ela, _ = c.reference_backward(col(h))
     _near(col(got["x"]), dx, E, "dx")
     _near(col(got["log_a"]), dla, Ela, "dlog_a")
+
+
+@pytest.mark.parametrize("D", [64, 35])
+def test_many_packed_sequences(D):
+    """150 sequences of 0 to 600 tokens: more chains of tiles than are handed out by turns."""
+    g = torch.Generator().manual_seed(D)
+    c = Case(torch.randint(0, 601, (150,), generator=g).tolist(), D, dtype="bf16", packed=True)
+    h, last = c.forward()
+    ref, rl, E, el = c.reference()
+    _near(h, ref, E, "h")
+    _near(last, rl, el, "h_last")
+    got = binding.glr_backward(c.rows(c.la), h, c.rows(c.dh), h0=c.h0.to(DEV), dh_last=c.dl.to(DEV),
+                               cu_seqlens=c.cu, T=c.T)
+    dx, dla, d0, E, Ela, e0 = c.reference_backward(h.cpu())
+    _near(got["x"], dx, E, "dx")
+    _near(got["log_a"], dla, Ela, "dlog_a")
+    _near(got["h0"], d0, e0, "dh0")
+
+
+def test_the_librarys_buffer_and_a_callers_workspace():
+    """The C entry points without a workspace (the library's buffer, grown between the calls) and with
+    one full of noise give the bits of the binding's call; one that is too small or off a 256-byte
+    boundary is refused."""
+    import ctypes
+    lib, P = binding.lib(), lambda t: t.data_ptr()  # noqa: E731
+    for T in (300, 5000):
+        c = Case([T] * 3, 68, seed=T)
+        x, la, dh, h0 = c.rows(c.x), c.rows(c.la), c.rows(c.dh), c.h0.to(DEV)
+        want = binding.glr_forward(x, la, h0=h0)
+        grads = binding.glr_backward(la, want, dh, h0=h0)
+        n = binding.glr_workspace_bytes(3, T, 68)
+        noise = torch.randint(0, 256, (n + 256,), device=DEV).to(torch.uint8)
+        assert noise.data_ptr() % 256 == 0
+        s = torch.cuda.current_stream().cuda_stream
+        for ws, size in ((None, 0), (P(noise), n)):
+            h, g = torch.empty_like(want), [torch.empty_like(t) for t in (la, la, h0)]
+            assert lib.llattn_glr_fwd(binding.F32, P(x), P(la), P(h0), P(h), None, 3, T, 68, None, ws, size, s) == 0
+            assert lib.llattn_glr_bwd(P(la), P(h), P(h0), P(dh), None, P(g[0]), P(g[1]), P(g[2]), 3, T, 68, None,
+                                      ws, size, s) == 0
+            assert torch.equal(h, want)
+            for t, m in zip(g, ("x", "log_a", "h0")):
+                assert torch.equal(t, grads[m]), m
+        assert lib.llattn_glr_fwd(binding.F32, P(x), P(la), None, P(want), None, 3, T, 68, None, P(noise), n - 1, s) == 7
+        assert lib.llattn_glr_fwd(binding.F32, P(x), P(la), None, P(want), None, 3, T, 68, None,
+                                  ctypes.c_void_p(P(noise) + 16), n, s) == 7
+
+
+def test_calls_side_by_side():
+    """Four calls on four streams at once, each with scratch of its own: the bits of calls alone."""
+    cases = [Case([2500] * 4, 100 + 4 * i, seed=i) for i in range(4)]
+    dev = [(c.rows(c.x), c.rows(c.la), c.rows(c.dh), c.h0.to(DEV)) for c in cases]
+    want = [binding.glr_forward(x, la, h0=h0) for x, la, _, h0 in dev]
+    want_g = [binding.glr_backward(la, h, dh, h0=h0) for (x, la, dh, h0), h in zip(dev, want)]
+    streams = [torch.cuda.Stream() for _ in dev]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for (x, la, dh, h0), s in zip(dev, streams):
+            with torch.cuda.stream(s):
+                h = binding.glr_forward(x, la, h0=h0)
+                got.append((h, binding.glr_backward(la, h, dh, h0=h0)))
+        torch.cuda.synchronize()
+        for (h, g), w, wg in zip(got, want, want_g):
+            assert torch.equal(h, w)
+            for n in wg:
+                assert torch.equal(g[n], wg[n]), n
 
 
 def test_steps_continue_a_prompt_in_place():

@@ -13,7 +13,8 @@ Backward: z w - u t collects the same errors of inv twice and those of z (rotati
 summed heads, 32 u), and the sum t adds 127 u and one more inv: at most 512 u of
 inv (sum of |dy| over heads and pair * |w| + |u| sum |z w u|).
 dw: a sum of products over all rows whose longest chain of additions is at most 2048 long in any of
-the tested shapes, each product off by at most 128 u: 2304 u of sum |z u|.
+the tested shapes (a lane adds the rows of its turns, at most 40000 / 64 here, then 64 lanes, then
+partial sums of at most 296 CTAs), each product off by at most 128 u: 2304 u of sum |z u|.
 """
 import math
 
@@ -136,6 +137,8 @@ CASES = [
     (1000, 4, 1, 4, 64, 48, "interleaved", "l2", True, "f32", True),
     (3001, 8, 8, 8, 64, 64, "half", "rms", True, "bf16", False),
     (5, 64, 1, 64, 128, 128, "interleaved", "l2", False, "f32", False),
+    (20000, 2, 1, 2, 32, 16, "half", "l2", True, "bf16", True),      # many batches for each CTA
+    (2, 600, 300, 600, 32, 32, "half", "l2", False, "bf16", False),  # one token to a batch
 ]
 
 
