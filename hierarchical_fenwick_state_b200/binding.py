@@ -437,8 +437,12 @@ def _on_device(fn, dev, stream, where, args):
     """The C call `fn(*args, stream)` with `dev`, the tensors' device, current."""
     import torch
     C = torch._C
-    # torch.cuda.current_stream() builds a Stream object (4 us of a 10 us call); its raw handle will do
-    raw = stream.cuda_stream if stream is not None else C._cuda_getCurrentRawStream(dev.index)
+    if stream is None:   # (torch.cuda.current_stream() builds a Stream object, 4 us of a 10 us call)
+        raw = C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"stream must be on {dev}")
+    else:
+        raw = stream.cuda_stream
     if dev.index == C._cuda_getDevice():
         st = fn(*args, raw)
     else:
@@ -472,6 +476,15 @@ def _expect(t, name, dtype, shape, dev, contiguous=True):
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
+
+
+def _new(like, shape, stream, dtype=None):
+    """An uninitialised result, which torch hands on in the order of the stream that writes it."""
+    import torch
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _expect_state(t, name, n, dev):
@@ -550,7 +563,7 @@ def qk_norm_rope(q, k, *, wq=None, wk=None, pos=None, inv_freq=None, heads: Opti
     H = max(Gq, Gk) if heads is None else heads
     shape = q.shape[:-2] + (H, d)
     if out is None:
-        out = (q.new_empty(shape), q.new_empty(shape))
+        out = (_new(q, shape, stream), _new(q, shape, stream))
         o = (out[0].data_ptr(), out[1].data_ptr())
     else:
         o = (_expect(out[0], "out[0]", q.dtype, shape, dev), _expect(out[1], "out[1]", q.dtype, shape, dev))
@@ -576,11 +589,11 @@ def qk_norm_rope_backward(q, k, dqo, dko, *, wq=None, wk=None, pos=None, inv_fre
     shape = q.shape[:-2] + (H, d)
     dy = (_expect(dqo, "dqo", f32, shape, dev), _expect(dko, "dko", f32, shape, dev))
     if grads is None:
-        grads = {"q": dqo.new_empty(q.shape), "k": dqo.new_empty(k.shape)}
+        grads = {"q": _new(dqo, q.shape, stream), "k": _new(dqo, k.shape, stream)}
         if wq is not None:
-            grads["wq"] = torch.empty_like(wq)
+            grads["wq"] = _new(wq, (d,), stream)
         if wk is not None:
-            grads["wk"] = torch.empty_like(wk)
+            grads["wk"] = _new(wk, (d,), stream)
         dqs, dks = Gq * d, Gk * d
     else:
         _expect(grads["q"], "grads['q']", f32, q.shape, dev, contiguous=False)
@@ -641,16 +654,13 @@ def _glr_need(B, T, D):
 def _workspace(workspace, need, like, stream):
     """A call's scratch: the caller's, or torch's for this call alone (none where none is needed):
     (tensor, address, bytes).  like: an fp32 tensor on the call's device."""
-    import torch
     if workspace is not None:
+        if workspace.device != like.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need == 0:
         return None, None, 0
-    if stream is None:
-        ws = like.new_empty(need // 4)
-    else:
-        with torch.cuda.stream(stream):   # torch hands it on in that stream's order
-            ws = like.new_empty(need // 4)
+    ws = _new(like, need // 4, stream)
     return ws, ws.data_ptr(), need
 
 
@@ -671,7 +681,7 @@ def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[
     states = _expect_state(h0, "h0", B * D, dev), _expect_state(h_last, "h_last", B * D, dev)
     cu = _expect(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
     if out is None:
-        out = torch.empty_like(log_a)
+        out = _new(log_a, x.shape, stream)
     h = _expect(out, "out", f32, x.shape, dev)
     ws, at, size = _workspace(workspace, _glr_need(B, T, D), log_a, stream)
     _on_device(lib().llattn_glr_fwd, dev, stream, "llattn_glr_fwd",
@@ -695,9 +705,9 @@ def glr_backward(log_a, h, dh, *, h0=None, dh_last=None, cu_seqlens=None, T: Opt
            _expect_state(dh_last, "dh_last", B * D, dev))
     cu = _expect(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
     if grads is None:
-        grads = {"x": torch.empty_like(log_a), "log_a": torch.empty_like(log_a)}
+        grads = {"x": _new(log_a, shape, stream), "log_a": _new(log_a, shape, stream)}
         if h0 is not None:
-            grads["h0"] = torch.empty_like(h0)
+            grads["h0"] = _new(h0, h0.shape, stream)
     outs = (_expect(grads["x"], "grads['x']", f32, shape, dev),
             _expect(grads["log_a"], "grads['log_a']", f32, shape, dev),
             _expect_state(grads.get("h0"), "grads['h0']", B * D, dev))
@@ -775,7 +785,7 @@ def read_state_q8(state, B, H, L, dk, dv, slot=None, out=None, dtype=None, strea
     at = _expect(slot, "slot", torch.int32, (B,), dev)
     shape = (B, H, dk, dv) if slot is not None else (B, H, L - 1, dk, dv)
     if out is None:
-        out = state.new_empty(shape, dtype=dtype or torch.bfloat16)
+        out = _new(state, shape, stream, dtype or torch.bfloat16)
     o = _expect(out, "out", out.dtype, shape, dev)
     _on_device(lib().llattn_read_state_q8, dev, stream, "llattn_read_state_q8",
                (state.data_ptr(), at, o, _in_dtype(out), B, H, L, dk, dv))

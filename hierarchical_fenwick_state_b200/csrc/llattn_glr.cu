@@ -19,21 +19,24 @@
 //
 // What bounds it: memory traffic (10 bytes per element forward with bf16 x, 20 backward), as long
 // as enough CTAs are resident to hide a tile's chain of copy, join, look-back and store.  Three
-// CTAs of 256 threads with one tile each in flight carry 134 M elements in 262 us as one sequence
-// of 65536 steps and in 239 us as eight (5.1 and 5.6 TB/s); two CTAs with the next tile copied
-// ahead took 289 and 284 us, tiles held in registers 300 and 288, and clusters of eight CTAs that
-// walk a sequence side by side and pass the state through distributed shared memory 285 and 298:
-// they leave SMs idle at every shape that is no multiple of their waves.  With 32 channels a row
-// of a tile is one 128-byte line of log_a; 64 and 128 channels made fewer and larger tiles and no
-// better use of memory.
+// CTAs of 256 threads with one tile each in flight carry 134 M elements in 247 us as one sequence
+// of 65536 steps and in 239 us as eight (5.4 and 5.6 TB/s), and gradients of 79 M elements in eight
+// packed sequences in 337 us (4.7 TB/s).  Before tiles went by turns (below), when these three
+// CTAs took 262 and 239 us, two CTAs with the next tile copied ahead took 289 and 284, tiles held
+// in registers 300 and 288, and clusters of eight CTAs that walk a sequence side by side and pass
+// the state through distributed shared memory 285 and 298: they leave SMs idle at every shape that
+// is no multiple of their waves.  With 32 channels a row of a tile is one 128-byte line of log_a;
+// 64 and 128 channels made fewer and larger tiles and no better use of memory.
 //
 // Look-back.  A tile publishes its map (32 channels: one 16-byte record each, written and read
 // whole, so no fence is needed) before it knows what enters it.  Tiles are grouped by eight in
 // time: what enters tile k is the state that the last tile of the group before (in the first
-// group: the sequence's first tile) has published, carried through the maps of the group's earlier tiles in their order.  The grouping is fixed,
-// so the rounding is too: the same call gives the same bits, whichever tiles happen to be ready.
-// Tiles are handed out by a counter in an order in which a tile comes after all that it looks
-// back at, so those run or have run, and every wait ends (and is bounded all the same).
+// group: the sequence's first tile) has published, carried through the maps of the group's earlier
+// tiles in their order.  The grouping is fixed, so the rounding is too: the same call gives the
+// same bits, whichever tiles happen to be ready.  Tiles are numbered so that each comes after all
+// that it looks back at, and handed out in that order, by a counter or (see kFewChains) by turns
+// among CTAs that a cooperative launch keeps resident: those looked back at are in hand or done,
+// and every wait ends (and is bounded all the same).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -58,7 +61,7 @@ struct alignas(4 * VEC) Floats {
   float v[VEC];
 };
 // x as it lies in memory.  A lone bf16 cannot be copied asynchronously (4 bytes at least): the
-// aligned word around it is, and `odd` says which half it is.
+// aligned word that it lies in is, and `odd` says which half it is.
 template <typename T, int VEC>
 struct Raw;
 template <int VEC>
@@ -88,11 +91,21 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
+// (first: the tensor's first value)
 template <int VEC>
-__device__ __forceinline__ void copy_x(Raw<float, VEC>* dst, const float* src) { cp_async<4 * VEC>(dst, src); }
-__device__ __forceinline__ void copy_x(Raw<__nv_bfloat16, 4>* dst, const __nv_bfloat16* src) { cp_async<8>(dst, src); }
-__device__ __forceinline__ void copy_x(Raw<__nv_bfloat16, 1>* dst, const __nv_bfloat16* src) {
-  cp_async<4>(dst, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)3));
+__device__ __forceinline__ void copy_x(Raw<float, VEC>* dst, const float* src, const float*) { cp_async<4 * VEC>(dst, src); }
+__device__ __forceinline__ void copy_x(Raw<__nv_bfloat16, 4>* dst, const __nv_bfloat16* src, const __nv_bfloat16*) {
+  cp_async<8>(dst, src);
+}
+// A word's first half alone, or its second with the value before it: nothing behind the tensor's end
+// is read, and where its first value is a second half, nothing before it.
+__device__ __forceinline__ void copy_x(Raw<__nv_bfloat16, 1>* dst, const __nv_bfloat16* src, const __nv_bfloat16* first) {
+  const unsigned in = (unsigned)reinterpret_cast<uintptr_t>(src) & 2u;   // bytes into the word
+  if (in && src == first)
+    dst->w = (unsigned)__ldg(reinterpret_cast<const unsigned short*>(src)) << 16;
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_u32(dst)),
+                 "l"(reinterpret_cast<const char*>(src) - in), "r"(2u + in) : "memory");
 }
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -318,13 +331,13 @@ __global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch 
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         cp_async<4 * VEC>(&sm.a[s][tid], p.log_a + o + s * p.D);
-        copy_x(&sm.x[s][tid], xs + o + s * p.D);
+        copy_x(&sm.x[s][tid], xs + o + s * p.D, xs);
       }
     } else if (j.k >= 0) {   // steps past the end change nothing
       for (int s = 0; s < S; ++s) {
         if (s < n) {
           cp_async<4 * VEC>(&sm.a[s][tid], p.log_a + o + s * p.D);
-          copy_x(&sm.x[s][tid], xs + o + s * p.D);
+          copy_x(&sm.x[s][tid], xs + o + s * p.D, xs);
         } else {
           sm.a[s][tid] = Floats<VEC>{};
           sm.x[s][tid] = Raw<T, VEC>{};

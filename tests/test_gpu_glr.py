@@ -409,3 +409,35 @@ def test_binding_refusals():
         binding.glr_forward(x[0], x[0].clone(), cu_seqlens=torch.zeros(2, dtype=torch.int64, device=DEV), T=8)
     with pytest.raises(binding.LLAttnError):      # in place
         binding.glr_forward(x, x.clone(), out=x)
+
+
+def test_results_belong_to_the_stream_that_writes_them():
+    """A call on a side stream takes no memory that the current stream may still be writing; a
+    workspace of the host is refused."""
+    x, la = torch.randn((2, 700, 256), device=DEV), -torch.rand((2, 700, 256), device=DEV)
+    want = binding.glr_forward(x, la)
+    torch.cuda.synchronize()
+    s, busy = torch.cuda.Stream(), torch.empty_like(x)
+    at = busy.data_ptr()
+    for _ in range(50):
+        busy.fill_(1.0)
+    del busy                       # free for the current stream, whose fills are not done
+    h = binding.glr_forward(x, la, stream=s)
+    grads = binding.glr_backward(la, want, x, stream=s)
+    s.synchronize()
+    assert at not in (h.data_ptr(), grads["x"].data_ptr(), grads["log_a"].data_ptr())
+    assert torch.equal(h, want)
+    with pytest.raises(ValueError):
+        binding.glr_forward(x, la, workspace=torch.empty(1 << 20))
+
+
+@pytest.mark.parametrize("start", [0, 1])
+@pytest.mark.parametrize("T,D", [(17, 33), (333, 33), (1025, 1)])
+def test_lone_bf16_values_at_both_ends_of_a_word(start, T, D):
+    """Odd counts of bf16, from either half of a word: the first value, the last and those between."""
+    c = Case([T], D, dtype="bf16")
+    x = torch.full((T * D + 2,), float("nan"), dtype=torch.bfloat16, device=DEV)[start:start + T * D].view(1, T, D)
+    x.copy_(c.x.view(1, T, D))
+    la, h0 = c.la.to(DEV).view(1, T, D), c.h0.to(DEV)
+    h = binding.glr_forward(x, la, h0=h0)
+    assert torch.equal(h, binding.glr_forward(x.float(), la, h0=h0))   # bf16 values in fp32: the same

@@ -208,3 +208,13 @@ def test_binding_refuses_what_it_cannot_pass_on():
         binding.glr_forward(x, x)
     with pytest.raises(ValueError):
         binding.read_state_q8(torch.zeros(8, dtype=torch.uint8), 1, 1, 2, 32, 32)
+
+
+def test_workspace_is_checked():
+    import torch
+    like = torch.empty(4)
+    ws, at, size = binding._workspace(torch.empty(8), 16, like, None)
+    assert (at, size) == (ws.data_ptr(), 32)
+    for bad in (torch.empty(16)[::2], torch.empty(16, device="meta")):   # strided; of another device
+        with pytest.raises(ValueError):
+            binding._workspace(bad, 16, like, None)
