@@ -107,6 +107,27 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
   }
 }
 
+// (the same from shared memory, where ld_in's loads cannot go)
+__device__ __forceinline__ float at(const float* p) { return *p; }
+__device__ __forceinline__ float at(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void shared16(const float* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 u = reinterpret_cast<const float4*>(p)[i];
+    x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
+  }
+}
+__device__ __forceinline__ void shared16(const __nv_bfloat16* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+    const unsigned w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[8 * i + j] = __uint_as_float((j & 1) ? (w[j >> 1] & 0xffff0000u) : (w[j >> 1] << 16));
+  }
+}
+
 // Sixteen values, a block's half beside its other half on the neighbouring lane, as codes; returns
 // the block's exponent code.
 __device__ __forceinline__ unsigned store_codes(const uint64_t (&v)[8], int8_t* to) {
@@ -138,7 +159,8 @@ __device__ __forceinline__ unsigned store_codes(const uint64_t (&v)[8], int8_t* 
 
 // The step's CTA takes one 32-column block of one (head, sequence): thread (r, half) owns 16
 // columns of row r in every level.  Levels come lowest first, kStepBatch of them asked for at a
-// time, and those that the carry takes (slots 0..m-1) are the first m.
+// time, and those that the carry takes (slots 0..m-1) are the first m.  Latency bounds it: one sequence
+// of 16 heads of 128 x 128 takes 4.5 us, with a launch's 2.5 (the fp32 state's step 6.5).
 constexpr int kStepBatch = 8;
 
 template <typename Tin, int DK>
@@ -262,186 +284,338 @@ __global__ void __launch_bounds__(2 * DK, 640 / (2 * DK)) q8_step_kernel(Q8StepP
 
 // ---- the step of a large batch ----
 //
-// One CTA per (head, sequence) there: a whole slot is one run of dk * dv bytes, so one warp copies
-// the occupied slots, lowest first, to shared memory (a bulk copy each, the block exponents beside
-// it), kStages at a time, and the other warps read them out.  Bytes in flight wait in shared memory
-// in place of registers, which lets six CTAs of 64 x 64 states share an SM.
+// A CTA takes whole (head, sequence) pairs, one after another: a grid's CTA beyond those that fit
+// the machine is taken over by one that runs (clusterlaunchcontrol), so pairs of few slots and of
+// many even out.  One warp copies what pairs read, in their order, into two rings of shared memory:
+// a pair's rows (q, k, v, lam, gates) and its occupied slots, lowest first, a bulk copy of codes
+// each with the block exponents beside it.  It runs ahead of the others, which read the slots out,
+// by as much as the rings hold, over the ends of pairs too: memory stays busy while a pair's sums
+// are joined.
+//
+// What bounds it: 64 sequences of 32 heads of 64 x 64 (57 MB at positions over [0, 8192)) take 20 us, 2.9
+// TB/s, and of 128 x 128 (225 MB) 59 us, 3.8 TB/s.  While CTAs run, two thirds of the issue slots are
+// taken, by turning bytes into floats above all (28 instructions for 16 codes beside the 8 that sum
+// them), and a quarter of the shorter call is launch and tail.  One CTA per pair, its slots in a ring of
+// its own, took 23.5 and 96 us; half as many CTAs on an SM 21.6 with two rows to a reader and 23.8
+// with one; more do not fit the registers.
 template <int DK, int DV>
 struct Ring {
   static constexpr int kSlot = DK * DV, kExps = DK * (DV / 32);
-  static constexpr int kStages = kSlot <= 2048 ? 16 : kSlot <= 8192 ? 8 : 6;
   static constexpr int kChunks = kSlot / 16;
-  static constexpr int kThreads = kChunks / 2 < 64 ? 64 : kChunks / 2;   // readers
-  static constexpr int kRows = kChunks / kThreads;         // rows of a reader, 16 columns of each
+  static constexpr int kThreads = kChunks / 2;             // readers
+  static constexpr int kRows = 2;                          // rows of a reader, 16 columns of each
+  static constexpr int kPerSm = 512 / kThreads;            // CTAs that share an SM
+  static constexpr int kFit = 196 * 1024 / kPerSm / (kSlot + kExps), kStages = kFit < 16 ? kFit : 16;
   static constexpr int kBytes = kStages * (kSlot + kExps);
 };
 
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+// A pair's rows on their way through shared memory.
+template <typename Tin, int DK, int DV>
+struct alignas(16) PairRows {
+  Tin q[DK], k[DK], v[DV];
+  float lam[32], gate[32], la;
+  int n;                  // the position; kSkip: out of range, kEnd: no more pairs
+  unsigned bh;
+};
+constexpr int kSkip = -1, kEnd = -2;
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(const void* dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
 // The thread's copies so far arrive at the barrier when they are done.
 __device__ __forceinline__ void arrive_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
+// Asks for a CTA of the grid that has not started, to run its part here; the 16 bytes of the answer
+// arrive at the barrier.
+__device__ __forceinline__ void ask_for_cta(uint4* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+               ::"r"(ptx::smem_u32(answer)), "r"(ptx::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool got_cta(const uint4* answer, unsigned& x, unsigned& y) {
+  unsigned got, ax, ay;
+  asm volatile("{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+               "ld.shared.b128 a, [%3];\n\t"
+               "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+               "selp.b32 %0, 1, 0, p;\n\t"
+               "mov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+               "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t"
+               "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, a;\n\t}"
+               : "=&r"(got), "=&r"(ax), "=&r"(ay) : "r"(ptx::smem_u32(answer)) : "memory");
+  x = ax;
+  y = ay;
+  return got != 0u;
+}
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(Ring<DK, DV>::kThreads + 32, Ring<DK, DV>::kThreads == 128 ? 6 : 1) q8_step_ring_kernel(Q8StepProblem p) {
+struct RingShared {
+  static constexpr int NS = Ring<DK, DV>::kStages, kWarps = Ring<DK, DV>::kThreads / 32;
+  PairRows<Tin, DK, DV> rows[2];
+  float red[2][kWarps][DV];
+  uint4 answer;
+  uint64_t rows_full[2], rows_free[2], red_full[2], full[NS], free[NS], answered;
+};
+
+// The copying warp.  Its waits are bounded: after one that runs out it takes no more pairs, and it
+// leaves when its copies in flight have come.
+template <typename Tin, int DK, int DV>
+__device__ __forceinline__ void ring_copy(const Q8StepProblem& p, RingShared<Tin, DK, DV>& sh, int8_t* s_codes,
+                                          uint8_t* s_exps, int n) {
+  using R = Ring<DK, DV>;
+  using Rows = PairRows<Tin, DK, DV>;
+  const int lane = threadIdx.x & 31, nslot = p.L - 1;
+  unsigned h = blockIdx.x, b = blockIdx.y;
+  int st = 0, round = 0;                   // the next stage, and how often the ring was filled before it
+  bool ok = true;
+  for (int it = 0;; ++it) {
+    const int e = it & 1;
+    if (lane == 0) {
+      ptx::mbar_arrive_expect_tx(&sh.answered, 16);
+      ask_for_cta(&sh.answer, &sh.answered);
+    }
+    if (it >= 2) ok = ok && ptx::mbar_wait(&sh.rows_free[e], ((it >> 1) + 1) & 1);
+    if (!__all_sync(0xffffffffu, ok)) ok = false;
+    const bool in = n >= 0 && (nslot >= 31 || n < (1 << nslot));
+    unsigned u = in && ok ? (unsigned)n : 0u;
+    if (ok) {
+      const size_t bh = (size_t)b * p.H + h;
+      Rows& rows = sh.rows[e];
+      if (in) {
+        constexpr int kK = DK * sizeof(Tin) / 16, kV = DV * sizeof(Tin) / 16;
+        if (lane < kK) {
+          copy_async<16>(reinterpret_cast<char*>(rows.q) + lane * 16, static_cast<const char*>(p.q) + bh * DK * sizeof(Tin) + lane * 16);
+          copy_async<16>(reinterpret_cast<char*>(rows.k) + lane * 16, static_cast<const char*>(p.k) + bh * DK * sizeof(Tin) + lane * 16);
+        }
+        if (lane < kV)
+          copy_async<16>(reinterpret_cast<char*>(rows.v) + lane * 16, static_cast<const char*>(p.v) + bh * DV * sizeof(Tin) + lane * 16);
+        if (lane < p.L) copy_async<4>(&rows.lam[lane], p.lam + bh * p.L + lane);
+        if (lane < nslot) copy_async<4>(&rows.gate[lane], p.s.gate + (bh * 2 + (n & 1)) * nslot + lane);
+        if (lane == 0) copy_async<4>(&rows.la, p.log_a + bh);
+      }
+      arrive_copies(&sh.rows_full[e]);
+      if (lane == 0) {
+        if (!in) atomicOr(p.status, LLATTN_DEV_DECODE_POS);
+        rows.n = in ? n : kSkip;
+        rows.bh = (unsigned)bh;
+        arrive(&sh.rows_full[e]);
+      }
+      const int8_t* codes = p.s.codes + bh * nslot * R::kSlot;
+      const uint8_t* exps = p.s.exps + bh * nslot * R::kExps;
+      for (; u != 0u; u &= u - 1u) {
+        const int j = __ffs(u) - 1;
+        if (round > 0) ok = ptx::mbar_wait(&sh.free[st], (round + 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&sh.full[st], R::kSlot);
+          ptx::bulk_load(s_codes + st * R::kSlot, codes + (size_t)j * R::kSlot, R::kSlot, &sh.full[st]);
+        }
+        for (int x = lane * 8; x < R::kExps; x += 256)
+          copy_async<8>(s_exps + st * R::kExps + x, exps + (size_t)j * R::kExps + x);
+        arrive_copies(&sh.full[st]);
+        if (++st == R::kStages) {
+          st = 0;
+          ++round;
+        }
+      }
+    }
+    const bool came = ptx::mbar_wait(&sh.answered, it & 1);
+    const bool more = __all_sync(0xffffffffu, came) && got_cta(&sh.answer, h, b);
+    ok = ok && __all_sync(0xffffffffu, came);
+    if (!ok && lane == 0) atomicOr(p.status, LLATTN_DEV_WAIT_TIMEOUT);
+    if (!more || !ok) {
+      const int last = (it + 1) & 1;
+      if (it >= 1) ok = ptx::mbar_wait(&sh.rows_free[last], (((it + 1) >> 1) + 1) & 1) && ok;
+      if (__all_sync(0xffffffffu, ok)) {
+        arrive_copies(&sh.rows_full[last]);
+        if (lane == 0) {
+          sh.rows[last].n = kEnd;
+          arrive(&sh.rows_full[last]);
+        }
+      }
+      break;
+    }
+    n = __ldg(p.pos + b);
+    ptx::fence_proxy_async_smem();         // the answer is read before its place is written again
+    __syncwarp();
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  for (int i = 0; i < R::kStages; ++i) {   // every stage's last copy has come (at once but after a lost wait)
+    const int fills = round + (i < st ? 1 : 0);
+    if (fills > 0) ptx::mbar_wait(&sh.full[i], (fills + 1) & 1);
+  }
+}
+
+template <typename Tin, int DK, int DV>
+__global__ void __launch_bounds__(Ring<DK, DV>::kThreads + 32, Ring<DK, DV>::kPerSm) q8_step_ring_kernel(Q8StepProblem p) {
   using R = Ring<DK, DV>;
   constexpr int NT = R::kThreads, kWarps = NT / 32, CPR = DV / 16, NB = DV / 32, NS = R::kStages;
   extern __shared__ float4 ring_smem[];
   int8_t* s_codes = reinterpret_cast<int8_t*>(ring_smem);
   uint8_t* s_exps = reinterpret_cast<uint8_t*>(s_codes + NS * R::kSlot);
-  __shared__ uint64_t full;                // a batch of slots has come
-  __shared__ float s_lam[32], s_w[32], s_qk[kWarps];
-  __shared__ float s_red[kWarps][DV];
+  __shared__ RingShared<Tin, DK, DV> sh;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x, b = blockIdx.y, nslot = p.L - 1;
-  const int n = __ldg(p.pos + b);
-  const size_t bh = (size_t)b * p.H + h;
-  int8_t* codes = p.s.codes + bh * nslot * R::kSlot;
-  uint8_t* exps = p.s.exps + bh * nslot * R::kExps;
-  const int cc = tid % CPR, r0 = tid / CPR;            // a reader's 16 columns, its first row
-  const Tin* v = static_cast<const Tin*>(p.v) + bh * DV;
-  float qr[R::kRows], kr[R::kRows], la = 0.f, lam = 0.f;
-  if (warp < kWarps) {                     // on their way beside the position
-#pragma unroll
-    for (int r = 0; r < R::kRows; ++r) {
-      qr[r] = ld_in(static_cast<const Tin*>(p.q) + bh * DK + r0 + r * (NT / CPR));
-      kr[r] = ld_in(static_cast<const Tin*>(p.k) + bh * DK + r0 + r * (NT / CPR));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nslot = p.L - 1;
+  int n0 = 0;
+  if (warp == kWarps) n0 = __ldg(p.pos + blockIdx.y);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sh.rows_full[i], 33);   // the copying lanes' copies, and what its first lane writes
+      ptx::mbar_init(&sh.rows_free[i], kWarps);
+      ptx::mbar_init(&sh.red_full[i], kWarps);
     }
-    la = __ldg(p.log_a + bh);
-    if (tid < p.L) lam = __ldg(p.lam + bh * p.L + tid);
-  } else {
-    if (lane == 0) {
-      ptx::mbar_init(&full, 33);           // the copying lanes' small copies, and the bulk copies
-      ptx::fence_mbar_init();
+    for (int i = 0; i < NS; ++i) {
+      ptx::mbar_init(&sh.full[i], 33);        // the copying lanes' small copies, and the bulk copy
+      ptx::mbar_init(&sh.free[i], kWarps);
     }
-    __syncwarp();
+    ptx::mbar_init(&sh.answered, 1);
+    ptx::fence_mbar_init();
   }
-  if (n < 0 || (nslot < 31 && n >= (1 << nslot))) {
-    if (tid == 0) atomicOr(p.status, LLATTN_DEV_DECODE_POS);
-    return;
-  }
-  const unsigned un = (unsigned)n, par = un & 1u;
-  const int m = __ffs(~un) - 1, cnt = __popc(un);
-
-  if (warp == kWarps) {                    // the copying warp
-    unsigned u = un;
-    for (int left = cnt, batch = 0; left > 0 || batch == 0; left -= NS, ++batch) {
-      const int k = left < NS ? left : NS;
-      if (batch > 0)                       // the batch before is read (the readers' side: below)
-        asm volatile("bar.sync 3, %0;" ::"n"(NT + 32) : "memory");
-      if (lane == 0) ptx::mbar_arrive_expect_tx(&full, k * R::kSlot);
-      for (int st = 0; st < k; ++st, u &= u - 1u) {
-        const int j = __ffs(u) - 1;
-        if (lane == 0) ptx::bulk_load(s_codes + st * R::kSlot, codes + (size_t)j * R::kSlot, R::kSlot, &full);
-        for (int e = lane * 8; e < R::kExps; e += 256)
-          copy8(ptx::smem_u32(s_exps + st * R::kExps + e), exps + (size_t)j * R::kExps + e);
-      }
-      arrive_copies(&full);
-      if (batch == 0) asm volatile("bar.sync 1, %0;" ::"n"(NT + 32) : "memory");   // the barrier is there for all
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  if (warp == kWarps) {
+    ring_copy<Tin, DK, DV>(p, sh, s_codes, s_exps, n0);
     return;
   }
 
-  float* gate = p.s.gate + bh * 2 * nslot;
-  if (tid < p.L) s_lam[tid] = lam;
-  if (tid < nslot && ((un >> tid) & 1u)) s_w[tid] = expf(gate[par * nslot + tid] + la);
-  float qk = 0.f;
-#pragma unroll
-  for (int r = 0; r < R::kRows; ++r)
-    if (cc == 0) qk = fmaf(qr[r], kr[r], qk);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, o);
-  if (lane == 0) s_qk[warp] = qk;
-  uint64_t part[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) part[i] = 0ull;
-  asm volatile("bar.sync 1, %0;" ::"n"(NT + 32) : "memory");
-
-  unsigned u = un;
-  bool lost = false;
+  const int cc = tid % CPR, r0 = tid / CPR;   // a reader's 16 columns, its first row
   const int8_t* my_codes = s_codes + r0 * DV + cc * 16;
   const uint8_t* my_exps = s_exps + r0 * NB + (cc >> 1);
-  for (int left = cnt, batch = 0; left > 0; left -= NS, ++batch) {
-    const int k = left < NS ? left : NS;
-    if (batch > 0) asm volatile("bar.sync 3, %0;" ::"n"(NT + 32) : "memory");
-    if (!lost && !ptx::mbar_wait(&full, batch & 1)) {   // reported once; the values are unspecified then
-      lost = true;
-      atomicOr(p.status, LLATTN_DEV_WAIT_TIMEOUT);
+  int st = 0, ph = 0;
+  auto lost = [&] {                        // a wait ran out: the warp leaves, and so will those that wait for it
+    if (lane == 0) atomicOr(p.status, LLATTN_DEV_WAIT_TIMEOUT);
+  };
+  for (int it = 0;; ++it) {
+    const int e = it & 1;
+    if (!ptx::mbar_wait(&sh.rows_full[e], (it >> 1) & 1)) return lost();
+    const PairRows<Tin, DK, DV>& rows = sh.rows[e];
+    const int n = rows.n;
+    if (n == kEnd) return;
+    if (n == kSkip) {
+      __syncwarp();
+      if (lane == 0) arrive(&sh.rows_free[e]);
+      if (lane == 0) arrive(&sh.red_full[e]);
+      continue;
     }
-    for (int st = 0; st < k; ++st, u &= u - 1u) {
-      const int j = __ffs(u) - 1;
-      const float lw = s_w[j] * s_lam[j + 1];
+    const unsigned un = (unsigned)n, par = un & 1u;
+    const int m = __ffs(~un) - 1;
+    const size_t bh = rows.bh;
+    // lane j: the factor of slot j, and with its weight
+    const float la = rows.la, w = (un >> lane) & 1u ? expf(rows.gate[lane] + la) : 0.f;
+    const float lw = (un >> lane) & 1u ? w * rows.lam[lane + 1] : 0.f;
+    float qr[R::kRows];
+    uint64_t part[8], carry[R::kRows][8];
+    {
+      float x[16];
+      shared16(rows.v + cc * 16, x);
+#pragma unroll
+      for (int r = 0; r < R::kRows; ++r) {
+        qr[r] = at(rows.q + r0 + r * (NT / CPR));
+        const float kr = at(rows.k + r0 + r * (NT / CPR));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) carry[r][c] = pair(kr * x[2 * c], kr * x[2 * c + 1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[i] = 0ull;
+
+    for (int j = 0; j < m; ++j) {          // the slots that the carry takes
+      if (!ptx::mbar_wait(&sh.full[st], ph)) return lost();
+      const float wj = __shfl_sync(0xffffffffu, w, j), lwj = __shfl_sync(0xffffffffu, lw, j);
 #pragma unroll
       for (int r = 0; r < R::kRows; ++r) {
         uint64_t x[8];
         pairs16(*reinterpret_cast<const uint4*>(my_codes + st * R::kSlot + r * (NT / CPR) * DV), x);
-        const float f = qr[r] * q8_scale(my_exps[st * R::kExps + r * (NT / CPR) * NB]) * lw;
+        const float sc = q8_scale(my_exps[st * R::kExps + r * (NT / CPR) * NB]), f = qr[r] * sc * lwj, g = wj * sc;
+        const uint64_t f2 = pair(f, f), g2 = pair(g, g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          part[c] = fma2(f2, x[c], part[c]);
+          carry[r][c] = fma2(g2, x[c], carry[r][c]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&sh.free[st]);
+      if (++st == NS) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    if (m < nslot) {                       // the carried level, rounded to its blocks' powers of two
+      int8_t* codes = p.s.codes + (bh * nslot + m) * R::kSlot;
+      uint8_t* exps = p.s.exps + (bh * nslot + m) * R::kExps;
+#pragma unroll
+      for (int r = 0; r < R::kRows; ++r) {
+        const int row = r0 + r * (NT / CPR);
+        const unsigned ex = store_codes(carry[r], codes + row * DV + cc * 16);
+        if ((cc & 1) == 0) exps[row * NB + (cc >> 1)] = (uint8_t)ex;
+      }
+    }
+    for (unsigned u = m < 32 ? un >> m << m : 0u; u != 0u; u &= u - 1u) {
+      const int j = __ffs(u) - 1;
+      if (!ptx::mbar_wait(&sh.full[st], ph)) return lost();
+      const float lwj = __shfl_sync(0xffffffffu, lw, j);
+#pragma unroll
+      for (int r = 0; r < R::kRows; ++r) {
+        uint64_t x[8];
+        pairs16(*reinterpret_cast<const uint4*>(my_codes + st * R::kSlot + r * (NT / CPR) * DV), x);
+        const float f = qr[r] * q8_scale(my_exps[st * R::kExps + r * (NT / CPR) * NB]) * lwj;
         const uint64_t f2 = pair(f, f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) part[c] = fma2(f2, x[c], part[c]);
       }
-    }
-  }
-
-  // readout over the warp's 32 / CPR rows, halving the columns a lane carries, then over the warps
-  float x[16];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) unpair(part[c], x[2 * c], x[2 * c + 1]);
-  int first = 0;                           // the lane's first column of its 16
-#pragma unroll
-  for (int o = 16, k = 8; o >= CPR; o >>= 1, k >>= 1) {
-    const bool up = lane & o;
-    if (up) first += k;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (q >= k) break;
-      const float keep = up ? x[q + k] : x[q], send = up ? x[q] : x[q + k];
-      x[q] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < CPR / 2; ++q) s_red[warp][cc * 16 + first + q] = x[q];
-
-  // the carry into slot m, with slots 0..m-1 read once more: from their places in the ring, or where
-  // later slots have taken those from the L2 cache.  (Kept through the loop above the carry would
-  // cost a third of the CTAs that fit an SM.)
-  if (m < nslot) {
-    const bool held = cnt <= NS;
-    load16(v + cc * 16, x);
-#pragma unroll
-    for (int r = 0; r < R::kRows; ++r) {
-      const int row = r0 + r * (NT / CPR), at = row * DV + cc * 16, ea = row * NB + (cc >> 1);
-      uint64_t carry[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) carry[c] = pair(kr[r] * x[2 * c], kr[r] * x[2 * c + 1]);
-      for (int j = 0; j < m; ++j) {
-        uint64_t y[8];
-        pairs16(*reinterpret_cast<const uint4*>((held ? s_codes : codes) + (size_t)j * R::kSlot + at), y);
-        const float g = s_w[j] * q8_scale((held ? s_exps : exps)[(size_t)j * R::kExps + ea]);
-        const uint64_t g2 = pair(g, g);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) carry[c] = fma2(g2, y[c], carry[c]);
+      __syncwarp();
+      if (lane == 0) arrive(&sh.free[st]);
+      if (++st == NS) {
+        st = 0;
+        ph ^= 1;
       }
-      const unsigned e = store_codes(carry, codes + (size_t)m * R::kSlot + at);
-      if ((cc & 1) == 0) exps[(size_t)m * R::kExps + ea] = (uint8_t)e;
     }
-  }
-  asm volatile("bar.sync 2, %0;" ::"n"(NT) : "memory");
-  for (int c = tid; c < DV; c += NT) {
-    float s = 0.f, qkt = 0.f;
+
+    // readout over the warp's 32 / CPR rows, halving the columns a lane carries, then over the warps
+    float x[16];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      s += s_red[w][c];
-      qkt += s_qk[w];
+    for (int c = 0; c < 8; ++c) unpair(part[c], x[2 * c], x[2 * c + 1]);
+    int first = 0;                         // the lane's first column of its 16
+#pragma unroll
+    for (int o = 16, k = 8; o >= CPR; o >>= 1, k >>= 1) {
+      const bool up = lane & o;
+      if (up) first += k;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (q >= k) break;
+        const float keep = up ? x[q + k] : x[q], send = up ? x[q] : x[q + k];
+        x[q] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
     }
-    p.out[bh * DV + c] = fmaf(s_lam[0] * qkt, ld_in(v + c), s);
+#pragma unroll
+    for (int q = 0; q < CPR / 2; ++q) sh.red[e][warp][cc * 16 + first + q] = x[q];
+    __syncwarp();
+    if (lane == 0) arrive(&sh.red_full[e]);
+    if (warp < NB) {                       // 32 columns of the result each
+      float qk = 0.f;
+#pragma unroll
+      for (int i = lane; i < DK; i += 32) qk = fmaf(at(rows.q + i), at(rows.k + i), qk);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) qk += __shfl_xor_sync(0xffffffffu, qk, o);
+      if (!ptx::mbar_wait(&sh.red_full[e], (it >> 1) & 1)) return lost();
+      const int c = warp * 32 + lane;
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) s += sh.red[e][q][c];
+      p.out[bh * DV + c] = fmaf(rows.lam[0] * qk, at(rows.v + c), s);
+      if (warp == 0 && lane < nslot && (((un + 1u) >> lane) & 1u))
+        p.s.gate[(bh * 2 + (par ^ 1u)) * nslot + lane] = lane == m ? 0.f : rows.gate[lane] + la;
+    }
+    __syncwarp();
+    if (lane == 0) arrive(&sh.rows_free[e]);
   }
-  if (tid < nslot && (((un + 1u) >> tid) & 1u))
-    gate[(par ^ 1u) * nslot + tid] = (tid == m) ? 0.f : gate[par * nslot + tid] + la;
 }
 
 template <typename Tin, int DK, int DV>
@@ -461,24 +635,24 @@ cudaError_t launch_ring(const Q8StepProblem& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename Tin, int DK>
-cudaError_t launch_ring_dk(const Q8StepProblem& p, cudaStream_t st) {
-  switch (p.dv) {
-    case 32: return launch_ring<Tin, DK, 32>(p, st);
-    case 64: return launch_ring<Tin, DK, 64>(p, st);
-    default: return launch_ring<Tin, DK, 128>(p, st);
-  }
-}
-
-constexpr int kRingFrom = 2 * 148;   // (head, sequence) pairs from which they fill the machine
+// The step's ways.  A short launch of many small CTAs wins while the call is a wave or two of them; the
+// ring's CTAs, which go on from pair to pair, once it is longer and a slot is 4 KB at least.  By 64 x 64
+// and 128 x 128 states at positions over [0, 8192), us, without and with the ring: 288 pairs 6.2 and
+// 6.2, 16.2 and 12.6; 512 pairs 9.0 and 7.3, 27.3 and 20.1; 2048 pairs 23.8 and 20.3, 101 and 59; 8192
+// pairs of 64 x 64 89 and 62.  States of 32 x 32 take 10.4 and 11.3 at 2048 pairs, 24 and 28 at 8192.
+constexpr int kRingSlot = 4096;                 // codes of a slot, and
+constexpr long long kRingCodes = 1 << 21;       // of one slot of every pair, from which the ring is used
 
 template <typename Tin>
 cudaError_t launch_step(const Q8StepProblem& p, cudaStream_t st) {
-  if ((long long)p.B * p.H >= kRingFrom) {
-    switch (p.dk) {
-      case 32: return launch_ring_dk<Tin, 32>(p, st);
-      case 64: return launch_ring_dk<Tin, 64>(p, st);
-      default: return launch_ring_dk<Tin, 128>(p, st);
+  if (p.dk * p.dv >= kRingSlot && (long long)p.B * p.H * p.dk * p.dv >= kRingCodes) {
+    switch (p.dk * 1000 + p.dv) {
+      case 32128: return launch_ring<Tin, 32, 128>(p, st);
+      case 64064: return launch_ring<Tin, 64, 64>(p, st);
+      case 64128: return launch_ring<Tin, 64, 128>(p, st);
+      case 128032: return launch_ring<Tin, 128, 32>(p, st);
+      case 128064: return launch_ring<Tin, 128, 64>(p, st);
+      default: return launch_ring<Tin, 128, 128>(p, st);
     }
   }
   const dim3 grid(p.dv / 32, p.H, p.B);
@@ -503,11 +677,17 @@ cudaError_t launch_step(const Q8StepProblem& p, cudaStream_t st) {
 // in order, S = sum over pieces of exp(decay of the later pieces) S_piece, rounds and writes, and
 // sums the gates.  No order of arrival enters, so the same call gives the same bits.
 //
-// Arithmetic.  The products run on the tensor cores as mma.sync of bf16 with fp32 sums: the kernel
-// is bound by reading k and v once (512 bytes of fp32 or 256 of bf16 per 8192 operations at d = 64),
-// and a warp's 16 rows of S fit its registers.  f k is not a bf16: it goes in as three, the rounded
-// value and twice what the rounding left, which is all of fp32's bits; of fp32 inputs v does too, and
-// the three smallest of the nine products (2^-24 of the whole and less) are left out.
+// Arithmetic.  The products run on the tensor cores as mma.sync of bf16 with fp32 sums, and a warp's 16
+// rows of S fit its registers.  f k is not a bf16: it goes in as three, the rounded value and twice
+// what the rounding left, which is all of fp32's bits; of fp32 inputs v does too, and the three smallest
+// of the nine products (2^-24 of the whole and less) are left out.
+//
+// What bounds it: eight packed sequences of 77,000 tokens in all, 16 heads of 64 (326 MB of k, v and
+// log_a), take 122 us, 2.7 TB/s: the matrix instructions' pipe is busy for 60% of that, and the rest is
+// the chain from a stage's copy over the split to them.  With f k in two parts 110 us, but codes off by
+// up to 2e-4 of a step in place of 1.3e-5; four stages 125 us against three's 110, tiles of 16 and 64
+// tokens 116 and 122, 32 rows of S to a warp 109 (all with two parts).  Sums on the
+// CUDA cores, a token at a time, took 16 ms.
 constexpr int kPreTile = 32;       // tokens per stage
 constexpr int kPreStages = 3;
 constexpr int kPreSeg = 512;       // tokens whose factors are held at a time
@@ -822,7 +1002,8 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
 }
 
 // Joins the pieces of the buckets longer than one (grid: 1024-value part of the state x level above
-// ch_log, head, sequence) and writes the gates (one more CTA per head and sequence).
+// ch_log, head, sequence) and writes the gates (one more CTA per head and sequence).  Its CTAs start
+// while the sums are still being made and wait for them (a programmatic launch).
 constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(Q8PrefillProblem p, PreScratch ws, int parts) {
@@ -972,6 +1153,8 @@ cudaError_t launch_prefill(const Q8PrefillProblem& p, const PreScratch& s, cudaS
 }
 
 // ---- reading back: 16 values per thread ----
+// Bound by its stores (2 or 4 bytes for each code's one): all 15 slots of 16 heads of 64 x 64 of eight
+// sequences, 16 MB written, in 8.3 us.
 __device__ __forceinline__ void store16(float* o, const float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; i += 4)

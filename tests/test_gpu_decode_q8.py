@@ -94,10 +94,11 @@ POSITIONS = {
 @pytest.mark.parametrize("H,L,dk,dv,dtype", [
     (3, 14, 64, 64, "bf16"), (2, 17, 128, 128, "bf16"), (5, 5, 32, 32, "f32"), (1, 2, 64, 128, "f32"),
     (2, 14, 128, 32, "bf16"), (4, 5, 32, 128, "bf16"), (1, 32, 32, 32, "f32"),
-    # large batches (296 heads and sequences at least), whose slots go through a ring of 6, 8 or 16
+    # large batches, whose slots go through rings of 11, and (the smaller states) more CTAs than run at once
     (64, 14, 64, 64, "bf16"), (60, 17, 128, 128, "bf16"), (50, 5, 32, 32, "f32"), (100, 2, 64, 128, "f32"),
     (33, 14, 128, 32, "bf16"), (50, 5, 32, 128, "f32"), (75, 32, 32, 32, "f32"), (33, 14, 64, 32, "f32"),
-    (50, 5, 32, 64, "bf16"), (60, 17, 128, 64, "bf16"),
+    (50, 5, 32, 64, "bf16"), (60, 17, 128, 64, "bf16"), (60, 14, 128, 32, "bf16"), (110, 5, 32, 128, "f32"),
+    (128, 32, 64, 64, "f32"),
 ])
 def test_one_step(H, L, dk, dv, dtype):
     pos = torch.tensor(POSITIONS[L], dtype=torch.int32)
@@ -467,3 +468,37 @@ def test_binding_refusals():
                                  torch.zeros((B, 4, H), device=DEV), state, B, H, 4, L, d, d)
     with pytest.raises(TypeError):
         binding.read_state_q8(state, B, H, L, d, d, dtype=torch.float16)
+
+
+@pytest.mark.parametrize("B,H,dk,dv", [(43, 64, 64, 64), (30, 60, 32, 128), (41, 70, 32, 32), (9, 75, 128, 128)])
+def test_more_pairs_than_fit_the_machine(B, H, dk, dv):
+    """Sequences of every position, some out of range (left as they are), beyond what runs at once."""
+    L = 5
+    nslot = L - 1
+    g = torch.Generator().manual_seed(B)
+    pos = torch.arange(B, dtype=torch.int32) % 18 - 1      # -1 and 16 are out of range
+    good = (pos >= 0) & (pos < 16)
+    rnd = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    q, k, v = (rnd(B, H, n).to(torch.bfloat16) for n in (dk, dk, dv))
+    la, lam = -torch.exp(rnd(B, H) - 2), torch.nn.functional.softplus(rnd(B, H, L))
+    state, (codes, gate, exps) = _buffer(B, H, L, dk, dv)
+    codes.copy_(torch.randint(-127, 128, codes.shape, generator=g).to(torch.int8))
+    exps.copy_(torch.randint(110, 130, exps.shape, generator=g).to(torch.uint8))
+    gate.copy_(-30 * torch.rand(gate.shape, generator=g) ** 4)
+    before = state.clone()
+    S, gate0 = _values(codes, exps), gate.cpu().clone()
+    out = torch.full((B, H, dv), 7.0, device=DEV)
+    binding.device_status(clear=True)
+    binding.decode_step_q8(*[t.to(DEV) for t in (q, k, v, la, lam, pos)], state, out, B, H, L, dk, dv)
+    assert binding.device_status(clear=True) == DECODE_POS
+    ref, size, carry, csize, m = _step_ref(q[good].double(), k[good].double(), v[good].double(), la[good].double(),
+                                           lam[good].double(), pos[good], S[good], gate0[good].double(), L)
+    got = out.double().cpu()
+    assert bool(((got[good] - ref).abs() <= 256 * U * size).all())
+    assert bool((got[~good] == 7.0).all())
+    bc, _, be = _views(before, B, H, L, dk, dv)
+    for i, b in enumerate(torch.nonzero(good).flatten().tolist()):
+        if int(m[i]) < nslot:
+            _check_rounded(codes[b, :, m[i]], exps[b, :, m[i]], carry[i], 128 * U * csize[i], f"sequence {b}")
+    for b in torch.nonzero(~good).flatten().tolist():
+        assert torch.equal(codes[b], bc[b]) and torch.equal(exps[b], be[b]) and torch.equal(gate[b].cpu(), gate0[b])
