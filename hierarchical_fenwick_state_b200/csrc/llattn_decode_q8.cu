@@ -680,13 +680,16 @@ cudaError_t launch_step(const Q8StepProblem& p, cudaStream_t st) {
 // Arithmetic.  The products run on the tensor cores as mma.sync of bf16 with fp32 sums, and a warp's 16
 // rows of S fit its registers.  f k is not a bf16: it goes in as three, the rounded value and twice
 // what the rounding left, which is all of fp32's bits; of fp32 inputs v does too, and the three smallest
-// of the nine products (2^-24 of the whole and less) are left out.
+// of the nine products (2^-24 of the whole and less) are left out.  A matrix instruction cuts its sum
+// off where fp32 would round it, so the products of rounded values have sums of their own: one cut
+// per 16 tokens in place of three (1.7 codes in a million off by one, in place of 4.2; the bf16 products
+// of 16 tokens summed first and then added, rounded, are as exact and take 134 us against 123).
 //
 // What bounds it: eight packed sequences of 77,000 tokens in all, 16 heads of 64 (326 MB of k, v and
-// log_a), take 122 us, 2.7 TB/s: the matrix instructions' pipe is busy for 60% of that, and the rest is
-// the chain from a stage's copy over the split to them.  With f k in two parts 110 us, but codes off by
-// up to 2e-4 of a step in place of 1.3e-5; four stages 125 us against three's 110, tiles of 16 and 64
-// tokens 116 and 122, 32 rows of S to a warp 109 (all with two parts).  Sums on the
+// log_a), take 123 us, 2.7 TB/s: the matrix instructions' pipe is busy for 60% of that, and the rest is
+// the chain from a stage's copy over the split to them.  With f k in two parts it takes 110 us, but the
+// codes are 2e-4 off the exact ones, relative to their size, in place of 3e-5; with two parts four
+// stages took 125 us, tiles of 16 and 64 tokens 116 and 122, 32 rows of S to a warp 109.  Sums on the
 // CUDA cores, a token at a time, took 16 ms.
 constexpr int kPreTile = 32;       // tokens per stage
 constexpr int kPreStages = 3;
@@ -766,7 +769,7 @@ constexpr int pre_smem() {
   return kPreStages * (Tile<T, DK>::kBytes + Tile<T, DV>::kBytes);
 }
 
-// One warp's 16 rows of S over the 16 tokens from t0 of a tile: f[2t], f[2t+1], f[2t+8], f[2t+9]
+// One warp's 16 rows of S (the products of rounded values in acc, the others in sm) over the 16 tokens from t0 of a tile: f[2t], f[2t+1], f[2t+8], f[2t+9]
 // scale the lane's tokens.  The lane's places in a tile (the permutation repeats every 8 tokens)
 // are found once.  Products of one half of f k with all columns come before those of the other, so
 // that no two in a row wait for one another.
@@ -782,7 +785,7 @@ struct Walker<__nv_bfloat16, DK, DV> {
 #pragma unroll
     for (int n = 0; n < DV / 16; ++n) vo[n] = Tile<__nv_bfloat16, DV>::at(0u, (mi & 1) * 8 + r, 2 * n + (mi >> 1));
   }
-  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
+  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], float (&sm)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
                                        const float (&f)[4]) const {
     unsigned raw[4], kf[4][3], b[DV / 16][4];
     ldmatrix4t(raw, ks + t0 * (DK * 2) + ko);
@@ -794,7 +797,7 @@ struct Walker<__nv_bfloat16, DK, DV> {
     for (int q = 0; q < 3; ++q)
 #pragma unroll
       for (int n = 0; n < DV / 8; ++n)
-        mma_bf16(acc[n], kf[0][q], kf[1][q], kf[2][q], kf[3][q], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
+        mma_bf16(q ? sm[n] : acc[n], kf[0][q], kf[1][q], kf[2][q], kf[3][q], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
   }
 };
 
@@ -802,7 +805,7 @@ template <int DK, int DV>
 struct Walker<float, DK, DV> {
   int row, tok;
   __device__ __forceinline__ Walker(int warp, int lane) : row(16 * warp + (lane >> 2)), tok(2 * (lane & 3)) {}
-  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
+  __device__ __forceinline__ void step(float (&acc)[DV / 8][4], float (&sm)[DV / 8][4], uint32_t ks, uint32_t vs, int t0,
                                        const float (&f)[4]) const {
     using K = Tile<float, DK>;
     using V = Tile<float, DV>;
@@ -827,7 +830,7 @@ struct Walker<float, DK, DV> {
         for (int w = 0; w < 3 - q; ++w)
 #pragma unroll
           for (int n = 0; n < 4; ++n)
-            mma_bf16(acc[n0 + n], kf[0][q], kf[1][q], kf[2][q], kf[3][q], vp[n][0][w], vp[n][1][w]);
+            mma_bf16(q + w ? sm[n0 + n] : acc[n0 + n], kf[0][q], kf[1][q], kf[2][q], kf[3][q], vp[n][0][w], vp[n][1][w]);
     }
   }
 };
@@ -894,11 +897,11 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
   const T* k = static_cast<const T*>(p.k) + ((size_t)sp.start * p.H + h) * DK;
   const T* v = static_cast<const T*>(p.v) + ((size_t)sp.start * p.H + h) * DV;
   const float* la = p.log_a + (size_t)sp.start * p.H + h;
-  float acc[DV / 8][4];
+  float acc[DV / 8][4], sm[DV / 8][4];
 #pragma unroll
   for (int i = 0; i < DV / 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) acc[i][j] = sm[i][j] = 0.f;
   const Walker<T, DK, DV> walk(warp, lane);
   const Copier<T, DK, NT> kcopy(k, (size_t)p.H * DK, tid);
   const Copier<T, DV, NT> vcopy(v, (size_t)p.H * DV, tid);
@@ -955,11 +958,15 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
         const int at = tile * kPreTile + t0 + 2 * (lane & 3);
         const float2 fa = *reinterpret_cast<const float2*>(s_f + at), fb = *reinterpret_cast<const float2*>(s_f + at + 8);
         const float f[4] = {fa.x, fa.y, fb.x, fb.y};
-        walk.step(acc, ks, vs, t0, f);
+        walk.step(acc, sm, ks, vs, t0, f);
       }
     }
   }
 
+#pragma unroll
+  for (int i = 0; i < DV / 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] += sm[i][j];
   ptx::griddep_launch_dependents();       // the join's CTAs may come as these leave
   const size_t bh = (size_t)b * p.H + h;
   const int row = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
