@@ -69,6 +69,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -388,13 +393,13 @@ __device__ __forceinline__ void ring_copy(const Q8StepProblem& p, RingShared<Tin
       const size_t bh = (size_t)b * p.H + h;
       Rows& rows = sh.rows[e];
       if (in) {
-        constexpr int kK = DK * sizeof(Tin) / 16, kV = DV * sizeof(Tin) / 16;
+        constexpr int kPer = 16 / sizeof(Tin), kK = DK / kPer, kV = DV / kPer;
         if (lane < kK) {
-          copy_async<16>(reinterpret_cast<char*>(rows.q) + lane * 16, static_cast<const char*>(p.q) + bh * DK * sizeof(Tin) + lane * 16);
-          copy_async<16>(reinterpret_cast<char*>(rows.k) + lane * 16, static_cast<const char*>(p.k) + bh * DK * sizeof(Tin) + lane * 16);
+          copy_async<16>(rows.q + lane * kPer, static_cast<const Tin*>(p.q) + bh * DK + lane * kPer);
+          copy_async<16>(rows.k + lane * kPer, static_cast<const Tin*>(p.k) + bh * DK + lane * kPer);
         }
         if (lane < kV)
-          copy_async<16>(reinterpret_cast<char*>(rows.v) + lane * 16, static_cast<const char*>(p.v) + bh * DV * sizeof(Tin) + lane * 16);
+          copy_async<16>(rows.v + lane * kPer, static_cast<const Tin*>(p.v) + bh * DV + lane * kPer);
         if (lane < p.L) copy_async<4>(&rows.lam[lane], p.lam + bh * p.L + lane);
         if (lane < nslot) copy_async<4>(&rows.gate[lane], p.s.gate + (bh * 2 + (n & 1)) * nslot + lane);
         if (lane == 0) copy_async<4>(&rows.la, p.log_a + bh);
@@ -454,7 +459,8 @@ __device__ __forceinline__ void ring_copy(const Q8StepProblem& p, RingShared<Tin
 }
 
 template <typename Tin, int DK, int DV>
-__global__ void __launch_bounds__(Ring<DK, DV>::kThreads + 32, Ring<DK, DV>::kPerSm) q8_step_ring_kernel(Q8StepProblem p) {
+__global__ void __launch_bounds__(Ring<DK, DV>::kThreads + 32, Ring<DK, DV>::kPerSm)
+q8_step_ring_kernel(Q8StepProblem p) {
   using R = Ring<DK, DV>;
   constexpr int NT = R::kThreads, kWarps = NT / 32, CPR = DV / 16, NB = DV / 32, NS = R::kStages;
   extern __shared__ float4 ring_smem[];
@@ -713,6 +719,19 @@ __device__ __forceinline__ float bf16_hi(unsigned w) { return __uint_as_float(w 
 
 // (x, y) as three pairs: rounded, what the rounding left, rounded, and what that left (exact but for
 // fp32's last bits).
+__device__ __forceinline__ unsigned pack_bf16(uint64_t p) {
+  float x, y;
+  unpair(p, x, y);
+  return pack_bf16(x, y);
+}
+__device__ __forceinline__ void split3(uint64_t xy, unsigned (&part)[3]) {
+  const uint64_t minus = pair(-1.f, -1.f);
+  part[0] = pack_bf16(xy);
+  xy = fma2(pair(bf16_lo(part[0]), bf16_hi(part[0])), minus, xy);
+  part[1] = pack_bf16(xy);
+  part[2] = pack_bf16(fma2(pair(bf16_lo(part[1]), bf16_hi(part[1])), minus, xy));
+}
+// (one by one: fewer registers)
 __device__ __forceinline__ void split3(float x, float y, unsigned (&part)[3]) {
   part[0] = pack_bf16(x, y);
   x -= bf16_lo(part[0]);
@@ -862,6 +881,22 @@ struct Copier {
   }
 };
 
+// Piece or short level y of a sequence of n tokens: its tokens [lo, hi) and slot; false where it has none.
+__device__ __forceinline__ bool find_piece(const PreScratch& ws, int y, int n, int& lo, int& hi, int& slot) {
+  if (y < ws.pieces) {
+    lo = y << ws.ch_log;
+    hi = lo + (1 << ws.ch_log);
+    if (hi > n) return false;
+    slot = 31 - __clz(n ^ lo);            // lo < n: the highest bit they differ in
+    return slot > ws.ch_log;              // a bucket of one piece is a short level's
+  }
+  slot = y - ws.pieces;
+  if (!((n >> slot) & 1)) return false;
+  lo = (n >> (slot + 1)) << (slot + 1);
+  hi = lo + (1 << slot);
+  return true;
+}
+
 // Grid: (head, piece or short level, sequence), heads first: adjacent CTAs read adjacent rows.
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, PreScratch ws) {
@@ -881,18 +916,7 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
   }
   const bool piece = (int)blockIdx.y < ws.pieces;
   int lo, hi, slot;
-  if (piece) {
-    lo = (int)blockIdx.y << ws.ch_log;
-    hi = lo + (1 << ws.ch_log);
-    if (hi > n) return;
-    slot = 31 - __clz(n ^ lo);            // lo < n: the highest bit they differ in
-    if (slot <= ws.ch_log) return;        // a bucket of one piece is a short level's
-  } else {
-    slot = (int)blockIdx.y - ws.pieces;
-    if (!((n >> slot) & 1)) return;
-    lo = (n >> (slot + 1)) << (slot + 1);
-    hi = lo + (1 << slot);
-  }
+  if (!find_piece(ws, (int)blockIdx.y, n, lo, hi, slot)) return;
   const uint32_t s0 = (uint32_t)__cvta_generic_to_shared(pre_smem_raw);
   const T* k = static_cast<const T*>(p.k) + ((size_t)sp.start * p.H + h) * DK;
   const T* v = static_cast<const T*>(p.v) + ((size_t)sp.start * p.H + h) * DV;
@@ -1006,6 +1030,246 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
       }
       if ((lane & 3) == 0) p.s.exps[(at * DK + rr) * NB + blk] = (uint8_t)e;
     }
+}
+
+// ---- the same for bf16 at d_v = 128, d_k of 64 and 128: tcgen05 ----
+//
+// A CTA takes 64 rows of S (a slab of k's columns).  f k goes to shared memory in its three parts, a
+// token's 64 values a row of 128 bytes (the swizzled MN-major form), v beside it; D = A^T B with
+// A = [rounded; second part] stacked as 128 rows, and once more with the third part, each with
+// accumulators of its own in tensor memory, so parts are summed apart as above.  k comes two tiles ahead
+// in registers (each thread scales what it loaded itself), v one tile ahead.
+//
+// Against mma.sync (us): 128 x 128 states of 16 heads, one prompt of 65535 tokens 215 and 351, four of 8192
+// 133 and 178, one of 511 15.6 and 19.7, eight of 300 57 and 53; 64 x 128, four of 8191 85 and 103, two of
+// 2047 28 and 27.  At d_v = 64 (three CTAs to an SM) it gains nothing: 64 x 64, four of 8192 50 and 49, of
+// 4096 35 and 30; 128 x 64, four of 8191 102 and 103.  Issue slots and shared memory, which
+// takes the parts and gives them to the matrix instructions, are half busy each; the rest is the chain
+// from loading over scaling to the sums' end, with two CTAs on an SM.
+constexpr int kTcTok = 64;                            // tokens of a tile
+constexpr uint32_t kTcTile = kTcTok * 128;            // bytes of 64 columns of it
+constexpr uint32_t kTcParts = 3 * kTcTile;
+constexpr int kTcSeg = 256;                           // tokens whose factors are held
+constexpr int kTcThreads = 256;
+constexpr int kTcDv = 128, kTcPerSm = 2;
+constexpr uint32_t kTcV = kTcTile * (kTcDv / 64);     // bytes of a tile of v
+constexpr uint32_t kTcSmem = 2 * kTcParts + 3 * kTcV + 1024;   // and the way to a multiple of 1024
+
+__global__ void __launch_bounds__(kTcThreads, kTcPerSm)
+q8_prefill_tc_kernel(Q8PrefillProblem p, PreScratch ws, int slabs) {
+  constexpr int DV = kTcDv, HALF = DV / 2, NB = DV / 32, NW = kTcThreads / 32, KU = 512 / kTcThreads, VU = 64 * DV / 8 / kTcThreads,
+                kSegTiles = kTcSeg / kTcTok, kRow = HALF + 1;
+  static_assert(kTcSeg == kTcThreads, "a token's factor each");
+  static_assert(128 * kRow * 4 <= 2 * kTcParts, "the rows' exchange takes the parts' place");
+  constexpr uint32_t kIdesc = ptx::idesc_bf16(128, DV, 1, 1);
+  extern __shared__ uint8_t tc_smem_raw[];
+  __shared__ float s_f[kTcSeg], s_sum[NW];
+  __shared__ uint64_t done[2];
+  __shared__ uint32_t s_tmem;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x / slabs, slab = blockIdx.x % slabs, b = blockIdx.z, nslot = p.L - 1;
+  const SeqSpan sp = seq_span(b, p.T, p.cu_seqlens, p.status);
+  const int n = sp.len;
+  if (nslot < 31 && n >= (1 << nslot)) {
+    if (blockIdx.y == 0 && blockIdx.x == 0 && tid == 0) atomicOr(p.status, LLATTN_DEV_DECODE_POS);
+    return;
+  }
+  int lo, hi, slot;
+  if (!find_piece(ws, (int)blockIdx.y, n, lo, hi, slot)) return;
+  const int tiles = (hi - lo + kTcTok - 1) / kTcTok;   // from hi back
+
+  uint8_t* sm = tc_smem_raw + ((1024u - (ptx::smem_u32(tc_smem_raw) & 1023u)) & 1023u);
+  const uint32_t s0 = ptx::smem_u32(sm), v0 = s0 + 2 * kTcParts;
+  if (warp == 0) {
+    ptx::tmem_alloc(&s_tmem, 2 * DV);
+    ptx::tmem_relinquish();
+  }
+  if (tid == 32) {
+    ptx::mbar_init(&done[0], 1);
+    ptx::mbar_init(&done[1], 1);
+    ptx::fence_mbar_init();
+  }
+  // A tile's rows are whole but for a bucket shorter than one, whose rows before lo are zeros.  This
+  // thread's pieces of 16 bytes are of rows row + 32 u of k, vrow + u * (rows a pass) of v.
+  const int row = tid >> 3, vrow = tid / (DV / 8), first = kTcTok * tiles - (hi - lo);
+  const uint32_t koff = row * 128 + (((tid & 7) ^ (row & 7)) << 4);
+  const int kstep = p.H * p.dk, vstep = p.H * DV;      // values from one token to the next
+  const size_t from = (size_t)(sp.start + hi) * p.H + h;   // (rows of the tile at tile 0: hi - 64 on)
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + from * p.dk + slab * 64 + (tid & 7) * 8;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + from * DV + tid % (DV / 8) * 8;
+  const float* la = p.log_a + (size_t)sp.start * p.H + h;
+
+  auto load_k = [&](uint4 (&r)[KU], int tile) {
+    const __nv_bfloat16* at = k + (long long)(row - (tile + 1) * kTcTok) * kstep;
+#pragma unroll
+    for (int u = 0; u < KU; ++u)
+      r[u] = tile < tiles && row + u * (kTcTok / KU) >= first
+                 ? __ldcs(reinterpret_cast<const uint4*>(at + (long long)(u * (kTcTok / KU)) * kstep))
+                 : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto copy_v = [&](int tile) {
+    if (tile < tiles) {
+      const __nv_bfloat16* at = v + (long long)(vrow - (tile + 1) * kTcTok) * vstep;
+      const int pc = tid % (DV / 8);
+      const uint32_t to = v0 + (tile % 3) * kTcV + (pc >> 3) * kTcTile + vrow * 128 + (((pc & 7) ^ (vrow & 7)) << 4);
+#pragma unroll
+      for (int u = 0; u < VU; ++u) {      // (rows a pass: a multiple of 8, so one place in each)
+        const int r = u * (kTcTok / VU);
+        if (vrow + r >= first) copy16(to + r * 128, at + (long long)r * vstep);
+        else zero16(to + r * 128);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float log = 0.f;                        // of this thread's token of the next segment
+  auto load_log = [&](int seg_hi) {
+    const int seg_lo = max(lo, seg_hi - kTcSeg);
+    log = seg_lo + tid < seg_hi ? __ldg(la + (size_t)(seg_lo + tid) * p.H) : 0.f;
+  };
+
+  uint4 k0[KU], k1[KU];
+  load_log(hi);
+  load_k(k0, 0);
+  copy_v(0);
+  load_k(k1, 1);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  float D = 0.f;                          // log decay from the segment's end to hi
+  bool lost = false;
+  auto sum_tile = [&](int c, uint4 (&kr)[KU]) {
+    const int seg_hi = hi - c / kSegTiles * kTcSeg, seg_lo = max(lo, seg_hi - kTcSeg);
+    if (c % kSegTiles == 0) {             // the segment's factors: suffix sums of log_a
+      float after = log;
+      if (seg_lo > lo) load_log(seg_lo);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, after, o);
+        if (lane + o < 32) after += y;
+      }
+      if (lane == 0) s_sum[warp] = after;
+      const float next = __shfl_down_sync(0xffffffffu, after, 1);
+      __syncthreads();
+      float rest = lane < 31 ? D + next : D, total = 0.f;   // of the tokens after this one
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float y = s_sum[w];
+        if (w > warp) rest += y;
+        total += y;
+      }
+      s_f[tid] = expf(rest);
+      D += total;
+      __syncthreads();
+    }
+    if (c >= 2 && !lost) lost = !ptx::mbar_wait(&done[c & 1], ((c >> 1) + 1) & 1);   // tile c - 2 is summed
+    copy_v(c + 1);
+    const uint32_t parts = s0 + (c & 1) * kTcParts;
+    const int at = hi - (c + 1) * kTcTok + row - seg_lo;
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      const float f = row + u * (kTcTok / KU) >= first ? s_f[at + u * (kTcTok / KU)] : 0.f;
+      const unsigned w[4] = {kr[u].x, kr[u].y, kr[u].z, kr[u].w};
+      const uint64_t f2 = pair(f, f);
+      unsigned part[4][3];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) split3(mul2(pair(bf16_lo(w[i]), bf16_hi(w[i])), f2), part[i]);
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     ::"r"(parts + q * kTcTile + koff + u * (kTcTok / KU) * 128), "r"(part[0][q]), "r"(part[1][q]),
+                     "r"(part[2][q]), "r"(part[3][q]) : "memory");
+    }
+    load_k(kr, c + 2);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");   // v of this tile
+    ptx::fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      ptx::tc_fence_after();
+      const uint64_t a01 = ptx::sdesc_sw128(parts, kTcTile, 1024), a2 = ptx::sdesc_sw128(parts + 2 * kTcTile, 0, 1024);
+      const uint64_t bd = ptx::sdesc_sw128(v0 + (c % 3) * kTcV, kTcTile, 1024);
+#pragma unroll
+      for (int x = 0; x < kTcTok / 16; ++x) {
+        const uint32_t more = (c > 0 || x > 0) ? 1u : 0u;
+        ptx::mma_ss(tmem, a01 + 128 * x, bd + 128 * x, kIdesc, more);
+        ptx::mma_ss(tmem + DV, a2 + 128 * x, bd + 128 * x, kIdesc, more);
+      }
+      ptx::mma_commit(&done[c & 1]);
+    }
+  };
+  for (int c = 0; c < tiles; c += 2) {    // (by twos: a register set waits for its own tile alone)
+    sum_tile(c, k0);
+    if (c + 1 < tiles) sum_tile(c + 1, k1);
+  }
+  const int z = tiles - 1;                // every sum is done when the last tile's is
+  if (!ptx::mbar_wait(&done[z & 1], (z >> 1) & 1)) lost = true;
+  if (lost) atomicOr(p.status, LLATTN_DEV_WAIT_TIMEOUT);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  ptx::griddep_launch_dependents();       // the join's CTAs may come as these leave
+  ptx::tc_fence_after();
+
+  // Row r of S is lane r (rounded part; third in the other accumulator) and lane 64 + r (second
+  // part): thread r writes the row's first columns, thread 64 + r the others, and they exchange what the
+  // other one needs through shared memory.
+  // (The first four warps do this, whole blocks of the codes to a thread.)
+  const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
+  float* s_x = reinterpret_cast<float*>(sm);
+  const bool second = warp >= 2, mine = warp < 4;
+  float x[HALF];
+#pragma unroll
+  for (int g = 0; g < HALF / 32; ++g) {
+    if (!mine) break;
+    float y[32], w[32];
+    // for the other thread
+    ptx::tmem_ld32(lanes + (second ? 0 : HALF) + 32 * g, y);
+    if (!second) ptx::tmem_ld32(lanes + DV + HALF + 32 * g, w);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s_x[tid * kRow + 32 * g + i] = second ? y[i] : y[i] + w[i];
+    ptx::tmem_ld32(lanes + (second ? HALF : 0) + 32 * g, y);
+    if (!second) ptx::tmem_ld32(lanes + DV + 32 * g, w);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[32 * g + i] = second ? y[i] : y[i] + w[i];
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 2 * DV);
+  }
+  if (!mine) return;
+#pragma unroll
+  for (int i = 0; i < HALF; ++i) x[i] += s_x[(tid ^ 64) * kRow + i];
+  const size_t bh = (size_t)b * p.H + h;
+  const int srow = slab * 64 + (tid & 63), col = second ? HALF : 0;
+  if ((int)blockIdx.y < ws.pieces) {
+    float* o = ws.sum + ((bh * ws.pieces + blockIdx.y) * p.dk + srow) * DV + col;
+#pragma unroll
+    for (int i = 0; i < HALF; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    if (tid == 0 && slab == 0) ws.piece_log[bh * ws.pieces + blockIdx.y] = D;
+    return;
+  }
+  if (tid == 0 && slab == 0) ws.short_log[bh * ws.shorts + slot] = D;
+  const size_t at = (bh * nslot + slot) * p.dk + srow;
+#pragma unroll
+  for (int g = 0; g < HALF / 32; ++g) {
+    unsigned top = 0u, w[8];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(x[32 * g + i]) & 0x7fffffffu);
+    const unsigned e = q8_exp(top);
+    const float inv = q8_inverse(e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i] |= (unsigned)(q8_code(x[32 * g + 4 * i + j], inv, e) & 0xff) << (8 * j);
+    }
+    uint4* o = reinterpret_cast<uint4*>(p.s.codes + at * DV + col + 32 * g);
+    o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    p.s.exps[at * NB + col / 32 + g] = (uint8_t)e;
+  }
 }
 
 // Joins the pieces of the buckets longer than one (grid: 1024-value part of the state x level above
@@ -1124,6 +1388,22 @@ PreScratch pre_scratch(void* ws, int B, int H, int T, int L, int dk, int dv) {
   return s;
 }
 
+cudaError_t launch_prefill_tc(const Q8PrefillProblem& p, const PreScratch& s, cudaStream_t st) {
+  static std::atomic<bool> allowed[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!allowed[dev].load()) {
+    e = cudaFuncSetAttribute(q8_prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
+    if (e != cudaSuccess) return e;
+    allowed[dev].store(true);
+  }
+  const int slabs = p.dk / 64;
+  q8_prefill_tc_kernel<<<dim3(p.H * slabs, s.pieces + s.shorts, p.B), kTcThreads, kTcSmem, st>>>(p, s, slabs);
+  return cudaGetLastError();
+}
+
 template <typename T, int DK, int DV>
 cudaError_t launch_prefill_one(const Q8PrefillProblem& p, const PreScratch& s, cudaStream_t st) {
   constexpr int smem = pre_smem<T, DK, DV>();
@@ -1146,7 +1426,9 @@ cudaError_t launch_prefill_dk(const Q8PrefillProblem& p, const PreScratch& s, cu
   switch (p.dv) {
     case 32: return launch_prefill_one<T, DK, 32>(p, s, st);
     case 64: return launch_prefill_one<T, DK, 64>(p, s, st);
-    default: return launch_prefill_one<T, DK, 128>(p, s, st);
+    default:
+      if constexpr (DK >= 64 && sizeof(T) == 2) return launch_prefill_tc(p, s, st);
+      else return launch_prefill_one<T, DK, 128>(p, s, st);
   }
 }
 

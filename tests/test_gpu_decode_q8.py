@@ -239,6 +239,10 @@ def _prompt_levels(k, v, la, s, n, lvl):
     ([66000], 1, 18, 32, 32, "bf16", "slow", False),        # a bucket of 512 pieces
     ([2048, 1500, 2047, 512], 64, 13, 32, 32, "bf16", "slow", True),   # pieces of 512
     ([5000, 4096], 1, 14, 64, 64, "f32", "slow", True),
+    # tiles of 64 tokens: buckets shorter than one, of one, of several; more tokens than a segment of factors
+    ([0, 1, 63, 64, 65, 127, 700], 2, 14, 128, 128, "bf16", "dist", True),
+    ([9000, 3000], 3, 15, 64, 128, "bf16", "slow", True), ([20000], 1, 16, 128, 128, "bf16", "slow", False),
+    ([33, 2047], 5, 12, 128, 128, "bf16", "strong", True),
 ])
 def test_prompt(lengths, H, L, dk, dv, dtype, gates, packed):
     k, v, la, cu, dev = _prompt(lengths, H, dk, dv, dtype, gates, packed)
@@ -502,3 +506,20 @@ def test_more_pairs_than_fit_the_machine(B, H, dk, dv):
             _check_rounded(codes[b, :, m[i]], exps[b, :, m[i]], carry[i], 128 * U * csize[i], f"sequence {b}")
     for b in torch.nonzero(~good).flatten().tolist():
         assert torch.equal(codes[b], bc[b]) and torch.equal(exps[b], be[b]) and torch.equal(gate[b].cpu(), gate0[b])
+
+
+@pytest.mark.parametrize("dk,dv,dtype", [(64, 64, "bf16"), (128, 128, "bf16"), (64, 128, "bf16"), (128, 128, "f32")])
+def test_prompts_do_not_reach_into_their_neighbours(dk, dv, dtype):
+    """A sequence between two of infinities and NaN holds the same levels as between two of numbers."""
+    lengths, H, L = [70, 37, 90], 2, 8
+    k, v, la, cu, dev = _prompt(lengths, H, dk, dv, dtype, "dist", True)
+    want, _ = _buffer(3, H, L, dk, dv)
+    got = want.clone()
+    binding.prefill_state_q8(*dev, want, 3, H, 90, L, dk, dv, cu_seqlens=cu.to(DEV))
+    at = torch.ones(sum(lengths), dtype=torch.bool, device=DEV)
+    at[70:107] = False
+    for t, bad in zip(dev, (math.nan, math.inf, math.nan)):
+        t[at] = bad
+    binding.prefill_state_q8(*dev, got, 3, H, 90, L, dk, dv, cu_seqlens=cu.to(DEV))
+    for x, y in zip(_views(got, 3, H, L, dk, dv), _views(want, 3, H, L, dk, dv)):
+        assert torch.equal(x[1].view(torch.uint8), y[1].view(torch.uint8))
