@@ -385,10 +385,11 @@ def test_positions_and_lengths_out_of_range():
     _check_rounded(c[0, :, 3], e[0, :, 3], S, 2.0 ** -13 * size, "cut")
 
 
-def test_other_stream_and_graph_replay():
+@pytest.mark.parametrize("B,H,d", [(3, 4, 64), (20, 40, 64), (12, 16, 128)])
+def test_other_stream_and_graph_replay(B, H, d):
     """A decoding loop replayed from a graph (its position advanced on the device), beside the same
-    loop on a stream: the same bits."""
-    B, H, L, d, T = 3, 4, 8, 64, 40
+    loop on a stream: the same bits, for few heads and sequences and for many."""
+    L, T = 8, 40
     g = torch.Generator().manual_seed(2)
     toks = [torch.randn((T, B, H, d), generator=g).to(DEV).bfloat16() for _ in range(3)]
     la = -torch.rand((T, B, H), generator=g).to(DEV)
@@ -523,3 +524,47 @@ def test_prompts_do_not_reach_into_their_neighbours(dk, dv, dtype):
     binding.prefill_state_q8(*dev, got, 3, H, 90, L, dk, dv, cu_seqlens=cu.to(DEV))
     for x, y in zip(_views(got, 3, H, L, dk, dv), _views(want, 3, H, L, dk, dv)):
         assert torch.equal(x[1].view(torch.uint8), y[1].view(torch.uint8))
+
+
+def test_steps_and_prompts_side_by_side():
+    """Steps of large batches, prompts and forwards of the attention on three streams at once: each the
+    bits that it gives alone."""
+    d, L, T = 128, 10, 500
+    g = torch.Generator().manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=g).to(DEV).bfloat16()  # noqa: E731
+    B, H = 16, 20                                                       # the steps'
+    toks = [rnd(6, B, H, d) for _ in range(3)]
+    la1, lam1 = -torch.rand((6, B, H), generator=g).to(DEV), torch.rand((6, B, H, L), generator=g).to(DEV)
+    pos = torch.arange(B, dtype=torch.int32, device=DEV) * 17
+    k, v, la = rnd(4, T, 8, d), rnd(4, T, 8, d), -torch.rand((4, T, 8), generator=g).to(DEV)
+    lam = torch.rand((4, T, 8, binding.num_levels(T)), generator=g).to(DEV)
+    q = (k / k.float().norm(dim=-1, keepdim=True)).bfloat16()
+
+    def steps(state, out):
+        for t in range(6):
+            binding.decode_step_q8(*(x[t] for x in toks), la1[t], lam1[t], pos + t, state, out[t], B, H, L, d, d)
+
+    def prompt(state):
+        for _ in range(6):
+            binding.prefill_state_q8(k, v, la, state, 4, 8, T, L, d, d)
+
+    def attention(out):
+        ws = torch.empty(binding.workspace_bytes(binding.BF16, "auto", 0, 4, 8, T, d, d, False), dtype=torch.uint8, device=DEV)
+        for _ in range(6):
+            binding.forward(q, q, v, la, lam, out=out, workspace=ws if ws.numel() else None)
+
+    held = torch.zeros(binding.decode_q8_state_bytes(B, H, L, d, d), dtype=torch.uint8, device=DEV)
+    empty = torch.zeros(binding.decode_q8_state_bytes(4, 8, L, d, d), dtype=torch.uint8, device=DEV)
+    res = []
+    for streams in ([torch.cuda.current_stream()] * 3, [torch.cuda.Stream() for _ in range(3)]):
+        a, b = held.clone(), empty.clone()
+        o1, o2 = torch.zeros((6, B, H, d), device=DEV), torch.zeros((4, T, 8, d), device=DEV)
+        torch.cuda.synchronize()
+        for st, f in zip(streams, (lambda: steps(a, o1), lambda: prompt(b), lambda: attention(o2))):
+            with torch.cuda.stream(st):
+                f()
+        torch.cuda.synchronize()
+        res.append((a, b, o1, o2))
+    assert binding.device_status(clear=True) == 0
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
