@@ -487,6 +487,15 @@ def _new(like, shape, stream, dtype=None):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _like(t, stream):
+    """The same, shaped as the contiguous tensor t (a third of new_empty's host time)."""
+    import torch
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _expect_state(t, name, n, dev):
     """The address of a contiguous fp32 tensor of n values that may be absent."""
     import torch
@@ -561,9 +570,10 @@ def qk_norm_rope(q, k, *, wq=None, wk=None, pos=None, inv_freq=None, heads: Opti
     wq, wk fp32 [d]; inv_freq fp32 [rot/2] with pos int32, one entry per token, or None."""
     dt, dev, n, Gq, Gk, d, rot, args = _qk_args(q, k, wq, wk, pos, inv_freq, norm, layout)
     H = max(Gq, Gk) if heads is None else heads
-    shape = q.shape[:-2] + (H, d)
+    shape = q.shape if H == Gq else q.shape[:-2] + (H, d)
     if out is None:
-        out = (_new(q, shape, stream), _new(q, shape, stream))
+        out = _new(q, shape, stream)
+        out = (out, _like(out, stream))
         o = (out[0].data_ptr(), out[1].data_ptr())
     else:
         o = (_expect(out[0], "out[0]", q.dtype, shape, dev), _expect(out[1], "out[1]", q.dtype, shape, dev))
@@ -586,14 +596,15 @@ def qk_norm_rope_backward(q, k, dqo, dko, *, wq=None, wk=None, pos=None, inv_fre
     if dqo.dim() < 3:
         raise ValueError("dqo must be [..., heads, d]")
     f32, H = torch.float32, dqo.shape[-2]
-    shape = q.shape[:-2] + (H, d)
+    shape = q.shape if H == Gq else q.shape[:-2] + (H, d)
     dy = (_expect(dqo, "dqo", f32, shape, dev), _expect(dko, "dko", f32, shape, dev))
     if grads is None:
-        grads = {"q": _new(dqo, q.shape, stream), "k": _new(dqo, k.shape, stream)}
+        grads = {"q": _like(dqo, stream) if H == Gq else _new(dqo, q.shape, stream),
+                 "k": _like(dko, stream) if H == Gk else _new(dqo, k.shape, stream)}
         if wq is not None:
-            grads["wq"] = _new(wq, (d,), stream)
+            grads["wq"] = _like(wq, stream)
         if wk is not None:
-            grads["wk"] = _new(wk, (d,), stream)
+            grads["wk"] = _like(wk, stream)
         dqs, dks = Gq * d, Gk * d
     else:
         _expect(grads["q"], "grads['q']", f32, q.shape, dev, contiguous=False)
@@ -681,7 +692,7 @@ def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[
     states = _expect_state(h0, "h0", B * D, dev), _expect_state(h_last, "h_last", B * D, dev)
     cu = _expect(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
     if out is None:
-        out = _new(log_a, x.shape, stream)
+        out = _like(log_a, stream)
     h = _expect(out, "out", f32, x.shape, dev)
     ws, at, size = _workspace(workspace, _glr_need(B, T, D), log_a, stream)
     _on_device(lib().llattn_glr_fwd, dev, stream, "llattn_glr_fwd",
@@ -705,9 +716,9 @@ def glr_backward(log_a, h, dh, *, h0=None, dh_last=None, cu_seqlens=None, T: Opt
            _expect_state(dh_last, "dh_last", B * D, dev))
     cu = _expect(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
     if grads is None:
-        grads = {"x": _new(log_a, shape, stream), "log_a": _new(log_a, shape, stream)}
+        grads = {"x": _like(log_a, stream), "log_a": _like(log_a, stream)}
         if h0 is not None:
-            grads["h0"] = _new(h0, h0.shape, stream)
+            grads["h0"] = _like(h0, stream)
     outs = (_expect(grads["x"], "grads['x']", f32, shape, dev),
             _expect(grads["log_a"], "grads['log_a']", f32, shape, dev),
             _expect_state(grads.get("h0"), "grads['h0']", B * D, dev))
