@@ -691,8 +691,8 @@ cudaError_t launch_step(const Q8StepProblem& p, cudaStream_t st) {
 // per 16 tokens in place of three (1.7 codes in a million off by one, in place of 4.2; the bf16 products
 // of 16 tokens summed first and then added, rounded, are as exact and take 134 us against 123).
 //
-// What bounds it: eight packed sequences of 77,000 tokens in all, 16 heads of 64 (326 MB of k, v and
-// log_a), take 123 us, 2.7 TB/s: the matrix instructions' pipe is busy for 60% of that, and the rest is
+// What bounds it: eight packed sequences of 92,500 tokens in all, 16 heads of 64 (385 MB of k, v and
+// log_a), take 123 us, 3.1 TB/s: the matrix instructions' pipe is busy for 60% of that, and the rest is
 // the chain from a stage's copy over the split to them.  With f k in two parts it takes 110 us, but the
 // codes are 2e-4 off the exact ones, relative to their size, in place of 3e-5; with two parts four
 // stages took 125 us, tiles of 16 and 64 tokens 116 and 122, 32 rows of S to a warp 109.  Sums on the

@@ -20,8 +20,8 @@
 // What bounds it: memory traffic (10 bytes per element forward with bf16 x, 20 backward), as long
 // as enough CTAs are resident to hide a tile's chain of copy, join, look-back and store.  Three
 // CTAs of 256 threads with one tile each in flight carry 134 M elements in 247 us as one sequence
-// of 65536 steps and in 239 us as eight (5.4 and 5.6 TB/s), and gradients of 79 M elements in eight
-// packed sequences in 337 us (4.7 TB/s).  Before tiles went by turns (below), when these three
+// of 65536 steps and in 239 us as eight (5.4 and 5.6 TB/s), and gradients of 95 M elements in eight
+// packed sequences in 337 us (5.6 TB/s).  Before tiles went by turns (below), when these three
 // CTAs took 262 and 239 us, two CTAs with the next tile copied ahead took 289 and 284, tiles held
 // in registers 300 and 288, and clusters of eight CTAs that walk a sequence side by side and pass
 // the state through distributed shared memory 285 and 298: they leave SMs idle at every shape that
