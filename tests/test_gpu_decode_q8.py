@@ -438,9 +438,9 @@ def test_the_librarys_buffer_and_a_callers_workspace():
                                                  n - 1, s) == 7
 
 
-def test_no_levels():
+@pytest.mark.parametrize("B,H,d", [(2, 3, 32), (32, 20, 64)])
+def test_no_levels(B, H, d):
     """L = 1: the token alone, no state."""
-    B, H, d = 2, 3, 32
     x = [torch.randn((B, H, d), device=DEV) for _ in range(3)]
     state = torch.empty(16, dtype=torch.uint8, device=DEV)
     out = torch.empty((B, H, d), device=DEV)
