@@ -688,8 +688,9 @@ cudaError_t launch_step(const Q8StepProblem& p, cudaStream_t st) {
 // what the rounding left, which is all of fp32's bits; of fp32 inputs v does too, and the three smallest
 // of the nine products (2^-24 of the whole and less) are left out.  A matrix instruction cuts its sum
 // off where fp32 would round it, so the products of rounded values have sums of their own: one cut
-// per 16 tokens in place of three (1.7 codes in a million off by one, in place of 4.2; the bf16 products
-// of 16 tokens summed first and then added, rounded, are as exact and take 134 us against 123).
+// per 16 tokens in place of three (two codes in a million off by one, in place of four; fp32 products and sums
+// give 2.4 to 3.4, and products of 16 tokens summed first and then added, rounded, 2, in 134 us against
+// 123).
 //
 // What bounds it: eight packed sequences of 92,500 tokens in all, 16 heads of 64 (385 MB of k, v and
 // log_a), take 123 us, 3.1 TB/s: the matrix instructions' pipe is busy for 60% of that, and the rest is
