@@ -1279,7 +1279,7 @@ q8_prefill_tc_kernel(Q8PrefillProblem p, PreScratch ws, int slabs) {
 constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(Q8PrefillProblem p, PreScratch ws, int parts) {
-  __shared__ float s_w[kJoinThreads], s_lvl[32];
+  __shared__ float s_lvl[32];
   ptx::griddep_wait();                    // the pieces are summed and visible
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, nslot = p.L - 1;
   const SeqSpan sp = seq_span(b, p.T, p.cu_seqlens, p.status);
@@ -1313,40 +1313,25 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(Q8PrefillProblem 
   const int first = bucket(slot), count = 1 << (slot - ws.ch_log), size = p.dk * p.dv;
   const float* src = ws.sum + (bh * ws.pieces + first) * size + part * 1024 + tid * 4;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  float later = 0.f;                      // log decay of the pieces behind the present ones
-  for (int c1 = count; c1 > 0; c1 -= kJoinThreads) {
-    const int c0 = max(0, c1 - kJoinThreads), m = c1 - c0;
-    const float4* from = reinterpret_cast<const float4*>(src + (size_t)c0 * size);
-    const size_t step = size / 4;
-    float4 x[8];                          // the last pieces are on their way while weights are made
+  float later = 0.f;                      // log decay of the pieces behind the present one
+  for (int c = count - 1; c >= 0; c -= 8) {   // (two pieces at least, a power of two)
+    float4 x[8];
+    float l[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < m) x[i] = __ldcs(from + (m - 1 - i) * step);
-    __syncthreads();
-    if (tid < m) s_w[tid] = logs[first + c0 + tid];
-    __syncthreads();
-    float w = 0.f;                        // (thread tid: the decay behind piece c0 + tid)
-    if (tid < m) {
-      w = later;
-      for (int c = tid + 1; c < m; ++c) w += s_w[c];
+    for (int i = 0; i < 8; ++i) {
+      if (i > c) break;
+      x[i] = __ldcs(reinterpret_cast<const float4*>(src + (size_t)(c - i) * size));
+      l[i] = logs[first + c - i];
     }
-    for (int c = 0; c < m; ++c) later += s_w[c];
-    __syncthreads();
-    if (tid < m) s_w[tid] = expf(w);
-    __syncthreads();
-    for (int c = m - 1; c >= 0; c -= 8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i > c) break;
-        const float f = s_w[c - i];
-        s.x = fmaf(f, x[i].x, s.x);
-        s.y = fmaf(f, x[i].y, s.y);
-        s.z = fmaf(f, x[i].z, s.z);
-        s.w = fmaf(f, x[i].w, s.w);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c - 8 - i >= 0) x[i] = __ldcs(from + (c - 8 - i) * step);
+    for (int i = 0; i < 8; ++i) {
+      if (i > c) break;
+      const float f = expf(later);
+      later += l[i];
+      s.x = fmaf(f, x[i].x, s.x);
+      s.y = fmaf(f, x[i].y, s.y);
+      s.z = fmaf(f, x[i].z, s.z);
+      s.w = fmaf(f, x[i].w, s.w);
     }
   }
   // eight threads hold a block of 32 values
