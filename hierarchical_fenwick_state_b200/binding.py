@@ -8,6 +8,7 @@ if the library is missing, ``lib()`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -769,6 +770,9 @@ def prefill_q8_workspace_bytes(B: int, H: int, T: int, L: int, dk: int, dv: int)
     return int(n.value)
 
 
+_prefill_q8_need = functools.lru_cache(maxsize=1024)(prefill_q8_workspace_bytes)   # (of the sizes alone)
+
+
 def prefill_state_q8(k, v, log_a, state, B, H, T, L, dk, dv, cu_seqlens=None, workspace=None,
                      stream=None):
     """llattn_prefill_state_q8: prefill_state into the 8-bit state.  k, v dense [B,T,H,d] or packed
@@ -782,7 +786,7 @@ def prefill_state_q8(k, v, log_a, state, B, H, T, L, dk, dv, cu_seqlens=None, wo
     cu = _expect(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
     if cu is not None and k.shape[0] == 0:
         T = 0                        # no rows at all: every sequence is empty
-    ws, at, size = _workspace(workspace, prefill_q8_workspace_bytes(B, H, T, L, dk, dv), log_a, stream)
+    ws, at, size = _workspace(workspace, _prefill_q8_need(B, H, T, L, dk, dv), log_a, stream)
     _on_device(lib().llattn_prefill_state_q8, dev, stream, "llattn_prefill_state_q8",
                (dt, *args, B, H, T, L, dk, dv, cu, at, size))
     return state
