@@ -9,8 +9,11 @@
 //
 // A gate of log_a = -inf (a = 0) starts the channel afresh at that token.
 //
-// Tiles.  n steps of a channel are the map y -> P y + H with P the product of their gates and H
-// the state they reach from 0, and maps of adjacent steps join as (P2 P1, P2 H1 + H2).  A CTA
+// Tiles.  n steps of a channel are the map y -> 2^G y + H with G the sum of their log2 gates and H
+// the state they reach from 0, and maps of adjacent steps join as (G2 + G1, 2^G2 H1 + H2).  The
+// product of the gates itself would leave fp32 where gates grow (128 steps of e) although the
+// state, or 0 that grows, does not.  A rounding of G is one of 2^G by at most |ln 2^G| 2^-24
+// relative, which for decaying gates is below 0.37 * 2^-24 of the entering state.  A CTA
 // takes tiles of 32 channels and TT steps: each thread walks S steps of its channels, copied to
 // its own places of shared memory, to their map; the threads' maps join over the warp (shuffles)
 // and the CTA (shared memory); the state that enters the tile comes from the tiles before it, and
@@ -19,13 +22,14 @@
 //
 // What bounds it: memory traffic (10 bytes per element forward with bf16 x, 20 backward), as long
 // as enough CTAs are resident to hide a tile's chain of copy, join, look-back and store.  Three
-// CTAs of 256 threads with one tile each in flight carry 134 M elements in 247 us as one sequence
-// of 65536 steps and in 239 us as eight (5.4 and 5.6 TB/s), and gradients of 95 M elements in eight
-// packed sequences in 337 us (5.6 TB/s).  Before tiles went by turns (below), when these three
-// CTAs took 262 and 239 us, two CTAs with the next tile copied ahead took 289 and 284, tiles held
-// in registers 300 and 288, and clusters of eight CTAs that walk a sequence side by side and pass
-// the state through distributed shared memory 285 and 298: they leave SMs idle at every shape that
-// is no multiple of their waves.  With 32 channels a row of a tile is one 128-byte line of log_a;
+// CTAs of 256 threads with one tile each in flight carry 134 M elements in 255 us as one sequence
+// of 65536 steps and in 248 us as eight (5.3 and 5.4 TB/s), and gradients of 95 M elements in eight
+// packed sequences in 326 us (5.8 TB/s).  With the plain product of gates in place of G, and before
+// tiles went by turns (below), three CTAs took 262 and 239 us forward, two CTAs with the next tile
+// copied ahead 289 and 284, tiles held in registers 300 and 288, and clusters of eight CTAs that
+// walk a sequence side by side and pass the state through distributed shared memory 285 and 298:
+// they leave SMs idle at every shape that is no multiple of their waves.  Maps joined value by value
+// in place of two by two take 264 and 260.  With 32 channels a row of a tile is one 128-byte line of log_a;
 // 64 and 128 channels made fewer and larger tiles and no better use of memory.
 //
 // Look-back.  A tile publishes its map (32 channels: one 16-byte record each, written and read
@@ -110,12 +114,88 @@ __device__ __forceinline__ void copy_x(Raw<__nv_bfloat16, 1>* dst, const __nv_bf
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // exp(x) as 2^(x log2 e): two instructions in place of nine.  Off by the rounding of the product
-// and of log2 e, 1.25 |x| 2^-24 relative, and two steps: what matters is a's own size, and |x| e^x
-// is below 0.37.  -inf gives 0, NaN stays.
-__device__ __forceinline__ float gate(float x) {
+// and of log2 e, 1.25 |x| 2^-24 relative, and two steps: for decaying gates what matters is a's own
+// size, and |x| e^x is below 0.37.  -inf (and less than -87.3) gives 0, NaN stays.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_of(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float gate(float x) { return exp2_of(x * kLog2e); }
+
+// VEC values at once, two by two: one instruction for a pair of products or sums.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+template <int N>
+__device__ __forceinline__ void add_to(float (&r)[N], const float (&x)[N]) {   // r + x
+  if constexpr (N == 1) r[0] += x[0];
+#pragma unroll
+  for (int i = 0; i + 1 < N; i += 2) {
+    uint64_t t;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(pair(r[i], r[i + 1])), "l"(pair(x[i], x[i + 1])));
+    unpair(t, r[i], r[i + 1]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void mul_by(float (&r)[N], const float (&x)[N]) {   // r x
+  if constexpr (N == 1) r[0] *= x[0];
+#pragma unroll
+  for (int i = 0; i + 1 < N; i += 2) {
+    uint64_t t;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(pair(r[i], r[i + 1])), "l"(pair(x[i], x[i + 1])));
+    unpair(t, r[i], r[i + 1]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void mul_by(float (&r)[N], float x) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = x;
+  mul_by(r, v);
+}
+template <int N>
+__device__ __forceinline__ void fma_to(float (&r)[N], const float (&a)[N], const float (&x)[N]) {   // a r + x
+  if constexpr (N == 1) r[0] = fmaf(a[0], r[0], x[0]);
+#pragma unroll
+  for (int i = 0; i + 1 < N; i += 2) {
+    uint64_t t;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(pair(a[i], a[i + 1])), "l"(pair(r[i], r[i + 1])), "l"(pair(x[i], x[i + 1])));
+    unpair(t, r[i], r[i + 1]);
+  }
+}
+
+// The maps (G, H) at y, 2^G y + H, in three factors: 2^G alone may be out of fp32's range (up to 2^277, the
+// ratio of its ends) where y and the result are in it.  A y of 0 stays 0 under any growth, and nothing is
+// left of any y behind a gate of 0.
+template <int N>
+__device__ __forceinline__ void apply(const float (&G)[N], const float (&H)[N], float (&y)[N]) {
+  float t[N], r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    t[i] = G[i];
+    r[i] = y[i];
+  }
+  mul_by(t, 1.f / 3);
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = exp2_of(t[i]);
+  mul_by(r, t);
+  mul_by(r, t);
+  fma_to(r, t, H);
+#pragma unroll
+  for (int i = 0; i < N; ++i) y[i] = t[i] > 0.f && y[i] != 0.f ? r[i] : H[i];
+}
+__device__ __forceinline__ float apply(float G, float H, float y) {
+  const float g[1] = {G}, h[1] = {H};
+  float r[1] = {y};
+  apply(g, h, r);
+  return r[0];
 }
 
 template <int VEC>
@@ -127,12 +207,12 @@ __device__ __forceinline__ void st_vec(float* p, const float (&v)[VEC]) {
 // What a tile has published of one channel: its map, and with kDone the state that leaves it.
 enum : unsigned { kNothing = 0u, kMap = 1u, kDone = 2u };
 struct alignas(16) Record {
-  float P, H, out;
+  float G, H, out;
   unsigned what;
 };
 
-__device__ __forceinline__ void publish(Record* r, float P, float H, float out, unsigned what) {
-  const uint64_t lo = (uint64_t)__float_as_uint(P) | ((uint64_t)__float_as_uint(H) << 32);
+__device__ __forceinline__ void publish(Record* r, float G, float H, float out, unsigned what) {
+  const uint64_t lo = (uint64_t)__float_as_uint(G) | ((uint64_t)__float_as_uint(H) << 32);
   const uint64_t hi = (uint64_t)__float_as_uint(out) | ((uint64_t)what << 32);
   asm volatile("{\n\t.reg .b128 q;\n\tmov.b128 q, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], q;\n\t}"
                ::"l"(r), "l"(lo), "l"(hi) : "memory");
@@ -205,64 +285,71 @@ __device__ __forceinline__ Job take_job(unsigned* next, unsigned& turn, unsigned
 template <int NT>
 struct Shared {
   struct {
-    float P[NT / 32][kCT], H[NT / 32][kCT];
-  } map[2];      // a warp may be a tile ahead of another's reading
+    float G[NT / 32][kCT], H[NT / 32][kCT];
+  } map[2];      // the warps' maps, then those of the warps before each (a warp may be a tile ahead)
   float in[kCT];
   Job job[4];    // a ring: the present tile, the next, the one being taken
 };
 
 // Joins the threads' maps of a tile (VEC channels of S steps each) over their warps, and the warps'
-// maps in shared memory; P, H come back as the map of the warp's slots before this one.
+// maps in shared memory; G, H come back as the map of the warp's slots before this one.
 template <int NT, int VEC>
-__device__ __forceinline__ void join_warps(Shared<NT>& sh, int it, float (&P)[VEC], float (&H)[VEC]) {
+__device__ __forceinline__ void join_warps(Shared<NT>& sh, int it, float (&G)[VEC], float (&H)[VEC]) {
   constexpr int LPR = kCT / VEC;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = (threadIdx.x % LPR) * VEC;
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1) {
+    float g[VEC], h[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      const float p = __shfl_up_sync(0xffffffffu, P[i], o), h = __shfl_up_sync(0xffffffffu, H[i], o);
-      if (lane >= o) {
-        H[i] = fmaf(P[i], h, H[i]);
-        P[i] *= p;
-      }
+      g[i] = __shfl_up_sync(0xffffffffu, G[i], o);
+      h[i] = __shfl_up_sync(0xffffffffu, H[i], o);
+    }
+    if (lane >= o) {
+      apply(G, H, h);
+      add_to(G, g);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) H[i] = h[i];
     }
   }
   if (lane >= 32 - LPR) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      sh.map[it & 1].P[warp][c0 + i] = P[i];
+      sh.map[it & 1].G[warp][c0 + i] = G[i];
       sh.map[it & 1].H[warp][c0 + i] = H[i];
     }
   }
   if constexpr (LPR < 32) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      P[i] = __shfl_up_sync(0xffffffffu, P[i], LPR);
+      G[i] = __shfl_up_sync(0xffffffffu, G[i], LPR);
       H[i] = __shfl_up_sync(0xffffffffu, H[i], LPR);
     }
   }
 }
 
-// The first warp, a lane per channel: finds what enters the tile (`start` where it is the
-// sequence's first), leaves it in sh.in and returns what leaves the tile.
+// The first warp, a lane per channel: joins the warps' maps, leaving with each those of the warps before
+// it, finds what enters the tile (`start` where it is the sequence's first), leaves it in sh.in and
+// returns what leaves the tile.
 template <int NT>
 __device__ __forceinline__ float look_back(Shared<NT>& sh, int it, const Job& at, float start, bool last,
                                            int nseq, int cts, Record* rec, unsigned int* status) {
   const int lane = threadIdx.x & 31;
-  float p = 1.f, h = 0.f, in = start;
+  float g = 0.f, h = 0.f, in = start;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    const float pw = sh.map[it & 1].P[w][lane];
-    h = fmaf(pw, h, sh.map[it & 1].H[w][lane]);
-    p *= pw;
+    const float gw = sh.map[it & 1].G[w][lane], hw = sh.map[it & 1].H[w][lane];
+    sh.map[it & 1].G[w][lane] = g;
+    sh.map[it & 1].H[w][lane] = h;
+    h = apply(gw, hw, h);
+    g += gw;
   }
   if (at.k > 0 || !last) {
     // records of this sequence and channel, by time tile
     const size_t step = (size_t)nseq * cts * kCT;
     Record* r = rec + ((size_t)at.b * cts + at.ct) * kCT + lane;
     if (at.k > 0) {
-      if (!last) publish(r + at.k * step, p, h, 0.f, kMap);
+      if (!last) publish(r + at.k * step, g, h, 0.f, kMap);
       // the tile whose outcome is taken (the sequence's first, or the last of the group before),
       // and the maps from there on: all asked for at once, those that were not there yet again
       const int base = max(at.k / kGroup * kGroup - 1, 0);
@@ -275,35 +362,31 @@ __device__ __forceinline__ float look_back(Shared<NT>& sh, int it, const Job& at
       for (int j = 0; j < kGroup - 1; ++j)
         if (base + 1 + j < at.k) {
           x[j] = wait_for(x[j], r + (base + 1 + j) * step, kMap, status);
-          in = fmaf(x[j].P, in, x[j].H);
+          in = apply(x[j].G, x[j].H, in);
         }
     }
-    if (!last) publish(r + at.k * step, p, h, fmaf(p, in, h), kDone);
+    if (!last) publish(r + at.k * step, g, h, apply(g, h, in), kDone);
   }
   sh.in[lane] = in;
-  return fmaf(p, in, h);
+  return apply(g, h, in);
 }
 
 // The value that enters this thread's steps: the tile's, through the warps and slots before.
 template <int NT, int VEC>
-__device__ __forceinline__ void enter(const Shared<NT>& sh, int it, const float (&P)[VEC],
+__device__ __forceinline__ void enter(const Shared<NT>& sh, int it, const float (&G)[VEC],
                                       const float (&H)[VEC], float (&mine)[VEC]) {
   constexpr int LPR = kCT / VEC;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = (threadIdx.x % LPR) * VEC;
+  float g[VEC], h[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) mine[i] = sh.in[c0 + i];
-#pragma unroll
-  for (int w = 0; w < NT / 32 - 1; ++w) {
-    if (w < warp) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) mine[i] = fmaf(sh.map[it & 1].P[w][c0 + i], mine[i], sh.map[it & 1].H[w][c0 + i]);
-    }
+  for (int i = 0; i < VEC; ++i) {
+    g[i] = sh.map[it & 1].G[warp][c0 + i];
+    h[i] = sh.map[it & 1].H[warp][c0 + i];
+    mine[i] = sh.in[c0 + i];
   }
+  apply(g, h, mine);
   if constexpr (LPR < 32) {
-    if (lane >= LPR) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) mine[i] = fmaf(P[i], mine[i], H[i]);
-    }
+    if (lane >= LPR) apply(G, H, mine);
   }
 }
 
@@ -358,26 +441,26 @@ __global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch 
     const float start = at.k == 0 && tid < 32 && cl < p.D && p.h0 ? p.h0[state] : 0.f;
     const long long o = (at.start + t0) * p.D + c;
     const unsigned odd = (unsigned)((reinterpret_cast<uintptr_t>(xs + o) >> 1) & 1);
-    float P[VEC], H[VEC], mine[VEC];
+    float G[VEC], H[VEC], mine[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      P[i] = 1.f;
-      H[i] = 0.f;
-    }
+    for (int i = 0; i < VEC; ++i) G[i] = H[i] = 0.f;
     cp_wait();
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       Floats<VEC> a = sm.a[s][tid];
-      const Raw<T, VEC> x = sm.x[s][tid];
+      const Raw<T, VEC> raw = sm.x[s][tid];
+      float x[VEC];
+      mul_by(a.v, kLog2e);
+      add_to(G, a.v);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        a.v[i] = gate(a.v[i]);
-        P[i] *= a.v[i];
-        H[i] = fmaf(a.v[i], H[i], x.get(i, (odd ^ (unsigned)(s * p.D)) & 1));
+        a.v[i] = exp2_of(a.v[i]);
+        x[i] = raw.get(i, (odd ^ (unsigned)(s * p.D)) & 1);
       }
+      fma_to(H, a.v, x);
       sm.a[s][tid] = a;
     }
-    join_warps<NT, VEC>(sh, it, P, H);
+    join_warps<NT, VEC>(sh, it, G, H);
     __syncthreads();
     if (tid == 32 && sh.job[(it + 1) & 3].k >= 0) sh.job[(it + 2) & 3] = take();
     if (tid < 32) {
@@ -385,16 +468,17 @@ __global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch 
       if (last && p.h_last && cl < p.D) p.h_last[state] = out;
     }
     __syncthreads();
-    enter<NT, VEC>(sh, it, P, H, mine);
+    enter<NT, VEC>(sh, it, G, H, mine);
     const int n = c < p.D ? at.len - t0 : 0;
     float* h = p.h + o;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const Floats<VEC> a = sm.a[s][tid];
-      const Raw<T, VEC> x = sm.x[s][tid];
+      const Raw<T, VEC> raw = sm.x[s][tid];
+      float x[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        mine[i] = fmaf(a.v[i], mine[i], x.get(i, (odd ^ (unsigned)(s * p.D)) & 1));
+      for (int i = 0; i < VEC; ++i) x[i] = raw.get(i, (odd ^ (unsigned)(s * p.D)) & 1);
+      fma_to(mine, a.v, x);
       if (s < n) st_vec<VEC>(h + s * p.D, mine);
     }
     copy(sh.job[(it + 1) & 3]);
@@ -455,26 +539,23 @@ __global__ void __launch_bounds__(NT, MINB) glr_bwd_tiles(GlrBwdProblem p, Scrat
     const bool last = (at.k + 1) * TT >= at.len;
     const long long state = (long long)at.b * p.D + cl;
     const float start = at.k == 0 && tid < 32 && cl < p.D && p.dh_last ? p.dh_last[state] : 0.f;
-    float P[VEC], H[VEC], mine[VEC];
+    float G[VEC], H[VEC], mine[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      P[i] = 1.f;
-      H[i] = 0.f;
-    }
+    for (int i = 0; i < VEC; ++i) G[i] = H[i] = 0.f;
     cp_wait();
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       Floats<VEC> a = sm.a[s][tid];
       const Floats<VEC> d = sm.dh[s][tid];
+      mul_by(a.v, kLog2e);
+      add_to(G, a.v);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        a.v[i] = gate(a.v[i]);
-        P[i] *= a.v[i];
-        H[i] = a.v[i] * (H[i] + d.v[i]);
-      }
+      for (int i = 0; i < VEC; ++i) a.v[i] = exp2_of(a.v[i]);
+      add_to(H, d.v);
+      mul_by(H, a.v);
       sm.a[s][tid] = a;
     }
-    join_warps<NT, VEC>(sh, it, P, H);
+    join_warps<NT, VEC>(sh, it, G, H);
     __syncthreads();
     if (tid == 32 && sh.job[(it + 1) & 3].k >= 0) sh.job[(it + 2) & 3] = take();
     if (tid < 32) {
@@ -482,23 +563,22 @@ __global__ void __launch_bounds__(NT, MINB) glr_bwd_tiles(GlrBwdProblem p, Scrat
       if (last && p.dh0 && cl < p.D) p.dh0[state] = out;
     }
     __syncthreads();
-    enter<NT, VEC>(sh, it, P, H, mine);
+    enter<NT, VEC>(sh, it, G, H, mine);
     const int n = c < p.D ? at.len - u0 : 0;
     const long long o = (at.start + at.len - 1 - u0) * p.D + c;
     float *dx = p.dx + o, *dla = p.dlog_a + o;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const Floats<VEC> a = sm.a[s][tid], d = sm.dh[s][tid], hp = sm.h[s][tid];
-      float g[VEC], dl[VEC];
+      const Floats<VEC> a = sm.a[s][tid];
+      Floats<VEC> g = sm.dh[s][tid], dl = sm.h[s][tid];
+      add_to(g.v, mine);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        g[i] = d.v[i] + mine[i];
-        mine[i] = a.v[i] * g[i];
-        dl[i] = mine[i] * hp.v[i];
-      }
+      for (int i = 0; i < VEC; ++i) mine[i] = g.v[i];
+      mul_by(mine, a.v);
+      mul_by(dl.v, mine);
       if (s < n) {
-        st_vec<VEC>(dx - s * p.D, g);
-        st_vec<VEC>(dla - s * p.D, dl);
+        st_vec<VEC>(dx - s * p.D, g.v);
+        st_vec<VEC>(dla - s * p.D, dl.v);
       }
     }
     copy(sh.job[(it + 1) & 3]);
@@ -637,6 +717,9 @@ cudaError_t fwd(const GlrProblem& p, void* ws, cudaStream_t st) {
   }
   const bool vec = p.D % 4 == 0 && aligned_to(p.x, 4 * sizeof(T)) && aligned_to(p.log_a, 16) &&
                    aligned_to(p.h, 16);
+  // Eight steps of four channels a thread: seven take 278 us for one sequence of 65536 x 2048, nine 257 (and
+  // 143 for 132 at 32 x 2048 x 1024, whose last tile is then short), twelve with two CTAs to an SM 257
+  // (and 271 for 258 at 8 x 8192 x 2048), six with three CTAs 289.
   if (!vec) return fwd_tiles<T, 128, 1, 32, 4>(p, ws, st);
   return fwd_tiles<T, 256, 4, 8, 3>(p, ws, st);
 }
@@ -662,8 +745,11 @@ cudaError_t glr_backward(const GlrBwdProblem& p, void* ws, cudaStream_t st) {
   const void* ptrs[6] = {p.log_a, p.h, p.h0, p.dh, p.dx, p.dlog_a};
   bool vec = p.D % 4 == 0;
   for (const void* q : ptrs) vec = vec && aligned_to(q, 16);
+  // Five steps a thread with three CTAs to an SM: 448 us for one sequence of 65536 x 2048 and 326 for the
+  // packed 95 M elements above; four steps 486 and 351, with four CTAs (whose registers spill) 515 and 371;
+  // six steps 497 and 368.
   if (!vec) return bwd_tiles<128, 1, 16, 6>(p, ws, st);
-  return bwd_tiles<256, 4, 4, 4>(p, ws, st);
+  return bwd_tiles<256, 4, 5, 3>(p, ws, st);
 }
 
 }  // namespace llattn

@@ -511,7 +511,9 @@ LLATTN_API llattn_status llattn_qk_norm_rope_bwd(
  *
  *   in_dtype   LLATTN_BF16 or LLATTN_F32: the type of x.
  *   x          [B, T, D] (packed: [total, D]); log_a the same shape, fp32, any sign; -inf starts
- *              a channel afresh at that token.
+ *              a channel afresh at that token.  A gate exp(log_a) is an fp32 number: infinite
+ *              from log_a = 88.8 on, 0 below -87.3.  Products of gates may leave fp32's range:
+ *              h is right wherever the sum of its terms' absolute values is in it.
  *   h0         fp32 [B, D], the state carried in, or NULL for 0.
  *   h          fp32 [.., D], fully overwritten for every token of every sequence (a packed
  *              sequence longer than T is cut at T, as in llattn_fwd; other rows are untouched).
