@@ -7,7 +7,8 @@
 //   g_t = dh_t + a_{t+1} g_{t+1}  (+ dh_last at the last t),
 //   dx_t = g_t,   dlog_a_t = g_t a_t h_{t-1},   dh0 = a_0 g_0.
 //
-// A gate of log_a = -inf (a = 0) starts the channel afresh at that token.
+// A gate of 0 (log_a = -inf) starts the channel afresh at that token: nothing of what was before enters,
+// an infinity or NaN included, and no gradient goes back.
 //
 // Tiles.  n steps of a channel are the map y -> 2^G y + H with G the sum of their log2 gates and H
 // the state they reach from 0, and maps of adjacent steps join as (G2 + G1, 2^G2 H1 + H2).  The
@@ -24,7 +25,7 @@
 // as enough CTAs are resident to hide a tile's chain of copy, join, look-back and store.  Three
 // CTAs of 256 threads with one tile each in flight carry 134 M elements in 255 us as one sequence
 // of 65536 steps and in 248 us as eight (5.3 and 5.4 TB/s), and gradients of 95 M elements in eight
-// packed sequences in 326 us (5.8 TB/s).  With the plain product of gates in place of G, and before
+// packed sequences in 332 us (5.7 TB/s).  With the plain product of gates in place of G, and before
 // tiles went by turns (below), three CTAs took 262 and 239 us forward, two CTAs with the next tile
 // copied ahead 289 and 284, tiles held in registers 300 and 288, and clusters of eight CTAs that
 // walk a sequence side by side and pass the state through distributed shared memory 285 and 298:
@@ -196,6 +197,20 @@ __device__ __forceinline__ float apply(float G, float H, float y) {
   float r[1] = {y};
   apply(g, h, r);
   return r[0];
+}
+
+// One step of the recurrence, and of the gradients' (c, in place of a (d + c)).
+__device__ __forceinline__ float step(float a, float h, float x) { return a == 0.f ? x : fmaf(a, h, x); }
+__device__ __forceinline__ float step_back(float a, float g) { return a == 0.f ? 0.f : a * g; }
+
+// Whether a log gate of -inf may be among a thread's, by their sums, which it makes -inf or NaN (lower
+// sums than -126 are few): its steps are then taken one by one, as above.
+template <int N>
+__device__ __forceinline__ bool may_cut(const float (&G)[N]) {
+  bool cut = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) cut |= !(G[i] > -126.f);
+  return cut;
 }
 
 template <int VEC>
@@ -460,6 +475,19 @@ __global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch 
       fma_to(H, a.v, x);
       sm.a[s][tid] = a;
     }
+    const bool cut = may_cut(G);
+    if (cut) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) H[i] = 0.f;
+#pragma unroll 1
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float a = sm.a[s][tid].v[i];
+          H[i] = step(a, H[i], sm.x[s][tid].get(i, (odd ^ (unsigned)(s * p.D)) & 1));
+          if (a == 0.f) G[i] = -INFINITY;
+        }
+    }
     join_warps<NT, VEC>(sh, it, G, H);
     __syncthreads();
     if (tid == 32 && sh.job[(it + 1) & 3].k >= 0) sh.job[(it + 2) & 3] = take();
@@ -471,15 +499,25 @@ __global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch 
     enter<NT, VEC>(sh, it, G, H, mine);
     const int n = c < p.D ? at.len - t0 : 0;
     float* h = p.h + o;
+    if (!cut) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const Floats<VEC> a = sm.a[s][tid];
-      const Raw<T, VEC> raw = sm.x[s][tid];
-      float x[VEC];
+      for (int s = 0; s < S; ++s) {
+        const Floats<VEC> a = sm.a[s][tid];
+        const Raw<T, VEC> raw = sm.x[s][tid];
+        float x[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) x[i] = raw.get(i, (odd ^ (unsigned)(s * p.D)) & 1);
-      fma_to(mine, a.v, x);
-      if (s < n) st_vec<VEC>(h + s * p.D, mine);
+        for (int i = 0; i < VEC; ++i) x[i] = raw.get(i, (odd ^ (unsigned)(s * p.D)) & 1);
+        fma_to(mine, a.v, x);
+        if (s < n) st_vec<VEC>(h + s * p.D, mine);
+      }
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < n && s < S; ++s) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          mine[i] = step(sm.a[s][tid].v[i], mine[i], sm.x[s][tid].get(i, (odd ^ (unsigned)(s * p.D)) & 1));
+        st_vec<VEC>(h + s * p.D, mine);
+      }
     }
     copy(sh.job[(it + 1) & 3]);
   }
@@ -555,6 +593,19 @@ __global__ void __launch_bounds__(NT, MINB) glr_bwd_tiles(GlrBwdProblem p, Scrat
       mul_by(H, a.v);
       sm.a[s][tid] = a;
     }
+    const bool cut = may_cut(G);
+    if (cut) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) H[i] = 0.f;
+#pragma unroll 1
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float a = sm.a[s][tid].v[i];
+          H[i] = step_back(a, sm.dh[s][tid].v[i] + H[i]);
+          if (a == 0.f) G[i] = -INFINITY;
+        }
+    }
     join_warps<NT, VEC>(sh, it, G, H);
     __syncthreads();
     if (tid == 32 && sh.job[(it + 1) & 3].k >= 0) sh.job[(it + 2) & 3] = take();
@@ -567,18 +618,34 @@ __global__ void __launch_bounds__(NT, MINB) glr_bwd_tiles(GlrBwdProblem p, Scrat
     const int n = c < p.D ? at.len - u0 : 0;
     const long long o = (at.start + at.len - 1 - u0) * p.D + c;
     float *dx = p.dx + o, *dla = p.dlog_a + o;
+    if (!cut) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const Floats<VEC> a = sm.a[s][tid];
-      Floats<VEC> g = sm.dh[s][tid], dl = sm.h[s][tid];
-      add_to(g.v, mine);
+      for (int s = 0; s < S; ++s) {
+        const Floats<VEC> a = sm.a[s][tid];
+        Floats<VEC> g = sm.dh[s][tid], dl = sm.h[s][tid];
+        add_to(g.v, mine);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) mine[i] = g.v[i];
-      mul_by(mine, a.v);
-      mul_by(dl.v, mine);
-      if (s < n) {
-        st_vec<VEC>(dx - s * p.D, g.v);
-        st_vec<VEC>(dla - s * p.D, dl.v);
+        for (int i = 0; i < VEC; ++i) mine[i] = g.v[i];
+        mul_by(mine, a.v);
+        mul_by(dl.v, mine);
+        if (s < n) {
+          st_vec<VEC>(dx - s * p.D, g.v);
+          st_vec<VEC>(dla - s * p.D, dl.v);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < n && s < S; ++s) {
+        float g[VEC], dl[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float a = sm.a[s][tid].v[i];
+          g[i] = sm.dh[s][tid].v[i] + mine[i];
+          mine[i] = step_back(a, g[i]);
+          dl[i] = a == 0.f ? 0.f : mine[i] * sm.h[s][tid].v[i];
+        }
+        st_vec<VEC>(dx - s * p.D, g);
+        st_vec<VEC>(dla - s * p.D, dl);
       }
     }
     copy(sh.job[(it + 1) & 3]);
@@ -602,7 +669,7 @@ __global__ void __launch_bounds__(kWalkThreads) glr_fwd_walk(GlrProblem p) {
 #pragma unroll 8
   for (int t = 0; t < sp.len; ++t) {
     const long long o = (long long)t * p.D;
-    h = fmaf(gate(__ldg(la + o)), h, ld_in(x + o));
+    h = step(gate(__ldg(la + o)), h, ld_in(x + o));
     out[o] = h;
   }
   if (p.h_last) p.h_last[at] = h;
@@ -620,9 +687,10 @@ __global__ void __launch_bounds__(kWalkThreads) glr_bwd_walk(GlrBwdProblem p) {
     const long long o = base + (long long)t * p.D;
     const float g = __ldg(p.dh + o) + back;
     const float past = t ? __ldg(p.h + o - p.D) : h0;
-    back = gate(__ldg(p.log_a + o)) * g;
+    const float a = gate(__ldg(p.log_a + o));
+    back = step_back(a, g);
     p.dx[o] = g;
-    p.dlog_a[o] = back * past;
+    p.dlog_a[o] = a == 0.f ? 0.f : back * past;
   }
   if (p.dh0) p.dh0[at] = back;
 }
@@ -745,7 +813,7 @@ cudaError_t glr_backward(const GlrBwdProblem& p, void* ws, cudaStream_t st) {
   const void* ptrs[6] = {p.log_a, p.h, p.h0, p.dh, p.dx, p.dlog_a};
   bool vec = p.D % 4 == 0;
   for (const void* q : ptrs) vec = vec && aligned_to(q, 16);
-  // Five steps a thread with three CTAs to an SM: 448 us for one sequence of 65536 x 2048 and 326 for the
+  // Five steps a thread with three CTAs to an SM: 457 us for one sequence of 65536 x 2048 and 332 for the
   // packed 95 M elements above; four steps 486 and 351, with four CTAs (whose registers spill) 515 and 371;
   // six steps 497 and 368.
   if (!vec) return bwd_tiles<128, 1, 16, 6>(p, ws, st);

@@ -511,7 +511,8 @@ LLATTN_API llattn_status llattn_qk_norm_rope_bwd(
  *
  *   in_dtype   LLATTN_BF16 or LLATTN_F32: the type of x.
  *   x          [B, T, D] (packed: [total, D]); log_a the same shape, fp32, any sign; -inf starts
- *              a channel afresh at that token.  A gate exp(log_a) is an fp32 number: infinite
+ *              a channel afresh at that token, whatever the state before it, infinities and NaN
+ *              included.  A gate exp(log_a) is an fp32 number: infinite
  *              from log_a = 88.8 on, 0 below -87.3.  Products of gates may leave fp32's range:
  *              h is right wherever the sum of its terms' absolute values is in it.
  *   h0         fp32 [B, D], the state carried in, or NULL for 0.
@@ -539,6 +540,8 @@ LLATTN_API llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float
  * gave it:
  *   g_t = dh_t + exp(log_a_{t+1}) g_{t+1}  (+ dh_last at the last token),
  *   dx_t = g_t,   dlog_a_t = g_t exp(log_a_t) h_{t-1},   dh0 = exp(log_a_0) g_0.
+ *   A token whose log_a is -inf passes nothing back: its dlog_a and what it adds to the gradient of
+ *   the token before are 0, whatever g and h are.
  *   log_a, h, dh   fp32 [.., D]; h0, dh_last fp32 [B, D] or NULL for 0.
  *   dx, dlog_a     fp32 [.., D], fully overwritten as h is in llattn_glr_fwd.
  *   dh0            fp32 [B, D] or NULL (not computed); dh_last for an empty sequence.

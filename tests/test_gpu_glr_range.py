@@ -130,3 +130,71 @@ def test_growth_and_decay_by_turns(B, T, D):
     back = size(dh.flip(1), torch.cat([torch.zeros_like(la[:, :1]), la.flip(1)[:, :-1]], 1), dl)
     scale = lambda t, f: (t.double() / f).float()  # noqa: E731
     _both(scale(x, fwd[:, None]), la, scale(h0, fwd), scale(dh, back[:, None]), scale(dl, back))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,T,D", [(3, 1, 8), (2, 9, 33)] + SHAPES)
+def test_nothing_crosses_a_start_afresh(B, T, D, dtype):
+    """Infinities and NaN in x, h0, dh and dh_last, and states that overflow, with log gates of -inf
+    behind (before) them: the rest of the channel is as if they were not there."""
+    g = torch.Generator().manual_seed(T * D)
+    x, dh = (torch.randn((B, T, D), generator=g) for _ in range(2))
+    la = -torch.exp(-2 + 0.5 * torch.randn((B, T, D), generator=g))
+    h0, dl = (torch.randn((B, D), generator=g) for _ in range(2))
+    u = torch.rand((B, T, D), generator=g)
+    cut = u < 4.0 / (T + 4)
+    la[cut] = -math.inf
+    la[:, 0, ::2] = -math.inf
+    bad = [math.inf, -math.inf, math.nan]
+    for t in (x, dh):
+        at = torch.rand((B, T, D), generator=g) < 1.0 / (T + 4)
+        t[at] = torch.tensor(bad)[torch.randint(3, (int(at.sum()),), generator=g)]
+    h0[:, ::3], dl[:, 1::3] = math.nan, math.inf
+    if T > 100:
+        la[:, 20:60, 2] = 4.0                  # e^160, then afresh
+        la[:, 60, 2], x[:, 20:61, 2] = -math.inf, 1.0
+    x = x.to(dtype)
+    a = la.double().exp()
+
+    def join(a, y, add, m, err, la):
+        zero = a == 0
+        cost = 16 * U + 48 * U * torch.where(zero, 0.0, la.double().abs())
+        y = torch.where(zero, 0.0, a * y) + add
+        m = torch.where(zero, 0.0, a * m) + add.abs()
+        err = torch.where(zero, 0.0, a * (err + TINY)) + cost * m
+        return y, m, err
+
+    def check(got, ref, tol, what):
+        got = got.double().cpu()
+        fits = ref.abs() < 2.0 ** 127          # (not for NaN)
+        assert bool(got[fits].isfinite().all()), what
+        assert bool(((got - ref).abs() <= tol + TINY)[fits].all()), what
+        assert not bool(got[ref.isnan()].isfinite().any()), what
+
+    last = torch.empty((B, D), device=DEV)
+    h = binding.glr_forward(x.to(DEV), la.to(DEV), h0=h0.to(DEV), h_last=last)
+    y, ref, E = h0.double(), torch.empty_like(a), torch.empty_like(a)
+    m, err = y.abs(), torch.zeros_like(y)
+    for t in range(T):
+        y, m, err = join(a[:, t], y, x[:, t].double(), m, err, la[:, t])
+        ref[:, t], E[:, t] = y, err
+    check(h, ref, E, "h")
+    check(last, ref[:, -1], E[:, -1], "h_last")
+
+    got = binding.glr_backward(la.to(DEV), h, dh.to(DEV), h0=h0.to(DEV), dh_last=dl.to(DEV))
+    hd, c = h.double().cpu(), dl.double()
+    m, err = c.abs(), torch.zeros_like(c)
+    dx, dla, Ex, Ela = (torch.empty_like(a) for _ in range(4))
+    for t in reversed(range(T)):
+        gt, m = dh[:, t].double() + c, dh[:, t].double().abs() + m
+        err = err + 16 * U * m + TINY
+        dx[:, t], Ex[:, t] = gt, err
+        past = hd[:, t - 1] if t else h0.double()
+        c, m, err = join(a[:, t], gt, torch.zeros_like(gt), m, err, la[:, t])
+        err = err + 48 * U * torch.where(a[:, t] == 0, 0.0, la[:, t].double().abs()) * m
+        zero = a[:, t] == 0
+        dla[:, t] = torch.where(zero, 0.0, c * past)
+        Ela[:, t] = torch.where(zero, 0.0, (err + 8 * U * m + TINY) * past.abs())
+    check(got["x"], dx, Ex, "dx")
+    check(got["log_a"], dla, Ela, "dlog_a")
+    check(got["h0"], c, err + 8 * U * m, "dh0")
