@@ -962,8 +962,9 @@ __global__ void __launch_bounds__(2 * DK) q8_prefill_kernel(Q8PrefillProblem p, 
       if (lane + o < 32) after += y;
     }
     if (lane == 0) s_sum[warp] = after;
+    const float next = __shfl_down_sync(0xffffffffu, after, 1);   // (after - run loses what a gate of 0 is behind)
     __syncthreads();
-    float rest = D + (after - run), total = 0.f;
+    float rest = lane < 31 ? D + next : D, total = 0.f;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
       const float y = s_sum[w];

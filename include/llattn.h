@@ -573,7 +573,8 @@ LLATTN_API llattn_status llattn_glr_bwd(const float* log_a, const float* h, cons
  *   aligned; 64 MB of sums at most where T <= 2^24 / (B*H), its contents do not matter), or NULL
  *   for the library's per-device buffer (as llattn_fwd: calls that overlap need their own).  The
  *   sums over a bucket run on the tensor cores with fp32 accumulation, every operand that is not a
- *   bf16 split into three; the same call gives the same bits.
+ *   bf16 split into three; the same call gives the same bits.  log_a is at most 0; -inf takes
+ *   what came before the token out of its bucket, and out of the read-outs of the levels before it.
  * llattn_read_state_q8 - the held values, as slots store them (their pending gates not applied),
  *   exactly for both types: slot NULL gives every slot, out [B, H, L-1, dk, dv] (slots that hold
  *   no level read as whatever they last held); a DEVICE int32 array slot [B] gives slot slot[b]
