@@ -342,7 +342,8 @@ prefill_kernel(PrefillProblem p) {
         const float y = __shfl_down_sync(0xffffffffu, x, o);
         if (tid + o < 32) x += y;
       }
-      s_f[tid] = __expf(D + (x - rla));
+      const float next = __shfl_down_sync(0xffffffffu, x, 1);   // (x - rla: NaN at a log a of -inf)
+      s_f[tid] = __expf(D + (tid < 31 ? next : 0.f));
       D += __shfl_sync(0xffffffffu, x, 0);
     }
 #pragma unroll

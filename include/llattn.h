@@ -345,7 +345,8 @@ LLATTN_API llattn_status llattn_decode_step(int in_dtype, const void* q, const v
  * contents (decoding never reads them).
  *   in_dtype  LLATTN_BF16 (k, v as uint16 bf16 bit patterns) or LLATTN_F32.
  *   k, v      DEVICE: dense [B, T, H, dk] / [B, T, H, dv], or packed [total, H, dk] /
- *             [total, H, dv] with cu_seqlens, as llattn_fwd takes them.  log_a [.., H] fp32.
+ *             [total, H, dv] with cu_seqlens, as llattn_fwd takes them.  log_a [.., H] fp32, at
+ *             most 0 (-inf takes what came before the token out of the state).
  *             q and lam are not needed: the state holds no readout.
  *   state     DEVICE fp32 buffer of llattn_decode_state_bytes(B, H, L, dk, dv), caller-owned,
  *             laid out as llattn_decode_step describes; the occupied level slots and all

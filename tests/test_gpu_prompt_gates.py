@@ -1,11 +1,12 @@
 """A prompt's hand-off to decoding with log gates of -inf and -1e5 among ordinary ones, inside buckets and
-behind them: on the 8-bit state (both of its kernels), and a step from there.
+behind them: on the 8-bit state (both of its kernels) and on the fp32 state, and a step from there.
 
 Bounds (u = 2^-24), in the terms' absolute values.  A term's decay is exp of a sum of at most 16 + 5 + 16
 roundings, each at most u of the sum D of the |log_a| behind the term (tokens in its bucket, up to the next gate of 0), and
 exp itself 4 u: (64 D + 4) u.  Products and sums: buckets of at most 1024 tokens are summed 16 at a
 time in pieces of at most 512, each time cut off at 2 u of the sum so far, at most 32 + 8 times, and the
-operands' parts leave 2^-24: 2^-17 in all.  A bucket's terms before a gate of 0 (exp of -inf or of -1e5) add
+operands' parts leave 2^-24: 2^-17 in all.  fp32 sums of the terms one by one, 128 or fewer to a
+CTA of a cluster, stay in that too.  A bucket's terms before a gate of 0 (exp of -inf or of -1e5) add
 nothing.  Held values are then rounded by half a step.
 """
 import math
@@ -90,4 +91,25 @@ def test_8_bit_state(dtype, dk, dv, mode):
     out = torch.empty((B, H, dv), device=DEV)
     binding.decode_step_q8(*(t.to(DEV) for t in (q, k1, v1, la1, lam, pos)), state, out, B, H, L, dk, dv)
     assert bool(((out.double().cpu() - want).abs() <= 256 * U * size).all())
+    assert binding.device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("mode", ["cut", "deep", "both"])
+@pytest.mark.parametrize("dtype,dk,dv", [("bf16", 64, 64), ("f32", 32, 128)])
+def test_fp32_state(dtype, dk, dv, mode):
+    B, H, L = len(LENGTHS), 2, 12
+    k, v, la, cu = _prompt(LENGTHS, H, dk, dv, dtype, mode)
+    state = torch.zeros(binding.decode_state_bytes(B, H, L, dk, dv) // 4, device=DEV)
+    n = B * H * (L - 1)
+    levels, gate = state[:n * dk * dv].view(B, H, L - 1, dk, dv), state[n * dk * dv:].view(B, H, 2, L - 1)
+    binding.prefill_state(k.to(DEV), v.to(DEV), la.to(DEV), state, B, H, max(LENGTHS), L, dk, dv,
+                          cu_seqlens=cu.to(DEV))
+    for b, m in enumerate(LENGTHS):
+        for j in range(L - 1):
+            if m >> j & 1:
+                S, err, rest, rerr = _level(k, v, la, int(cu[b]), m, j + 1)
+                got = levels[b, :, j].double().cpu()
+                assert bool(got.isfinite().all()) and bool(((got - S).abs() <= err + 2.0 ** -126).all()), (m, j)
+                got = gate[b, :, 0, j].double().cpu()
+                assert bool(((got == rest) | ((got - rest).abs() <= rerr)).all()), (m, j)
     assert binding.device_status(clear=True) == 0
