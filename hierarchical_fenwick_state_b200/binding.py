@@ -29,7 +29,8 @@ EXPORTS = (
     "llattn_bwd_workspace_bytes", "llattn_bwd", "llattn_fwd_bf16", "llattn_stream_status",
     "llattn_segment_plan", "llattn_set_segment_chunks", "llattn_gdn_fwd",
     "llattn_prefill_state", "llattn_qk_norm_rope", "llattn_qk_norm_rope_bwd_workspace_bytes",
-    "llattn_qk_norm_rope_bwd", "llattn_glr_workspace_bytes", "llattn_glr_fwd", "llattn_glr_bwd",
+    "llattn_qk_norm_rope_bwd", "llattn_glr_workspace_bytes",
+    "llattn_glr_packed_workspace_bytes", "llattn_glr_fwd", "llattn_glr_bwd",
     "llattn_decode_q8_state_bytes", "llattn_decode_step_q8",
     "llattn_prefill_q8_workspace_bytes", "llattn_prefill_state_q8",
     "llattn_read_state_q8",
@@ -112,6 +113,8 @@ def lib():
                                           ll, ll, f_p, f_p, ll, i, i, i, i, i, i, i, fl, vp, sz, vp]
     L.llattn_glr_workspace_bytes.restype = i
     L.llattn_glr_workspace_bytes.argtypes = [i, i, i, szp]
+    L.llattn_glr_packed_workspace_bytes.restype = i
+    L.llattn_glr_packed_workspace_bytes.argtypes = [i, i, ll, i, szp]
     L.llattn_glr_fwd.restype = i
     L.llattn_glr_fwd.argtypes = [i, vp, f_p, f_p, f_p, f_p, i, i, i, i_p, vp, sz, vp]
     L.llattn_glr_bwd.restype = i
@@ -644,7 +647,7 @@ def _glr_shape(t, cu_seqlens, T):
         if len(shape) < 2 or cu_seqlens.numel() < 1:
             raise ValueError("packed inputs are [total, ...channels] with cu_seqlens [B + 1]")
         B, D, rest = cu_seqlens.numel() - 1, shape[1], shape[2:]
-        T = T if shape[0] else 0   # no rows at all: every sequence is empty
+        T = min(T, shape[0])       # (no sequence is longer than all rows)
     for x in rest:
         D *= x
     return B, T, D
@@ -658,9 +661,20 @@ def glr_workspace_bytes(B: int, T: int, D: int) -> int:
     return int(n.value)
 
 
-def _glr_need(B, T, D):
-    """glr_workspace_bytes without the call (sizes that it refuses are refused by the operator)."""
-    return 0 if T <= 64 or B == 0 or D == 0 else 256 + -(-T // 64) * B * -(-D // 32) * 512
+def glr_packed_workspace_bytes(B: int, T: int, rows: int, D: int) -> int:
+    """The same for a packed batch of that many rows (llattn_glr_packed_workspace_bytes)."""
+    n = ctypes.c_size_t(0)
+    _check(lib().llattn_glr_packed_workspace_bytes(int(B), int(T), int(rows), int(D), ctypes.byref(n)),
+           "llattn_glr_packed_workspace_bytes")
+    return int(n.value)
+
+
+def _glr_need(B, T, D, rows=None):
+    """Either without the call (sizes that they refuse are refused by the operator)."""
+    if T <= 64 or B == 0 or D == 0:
+        return 0
+    slots = -(-T // 64) * B
+    return 256 + (slots if rows is None else min(slots, rows // 64 + B)) * -(-D // 32) * 512
 
 
 def _workspace(workspace, need, like, stream):
@@ -683,7 +697,8 @@ def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[
     x bf16 or fp32 and log_a fp32, both [B, T, ...channels], or [total, ...channels] with
     cu_seqlens and T.  h0 [B, ...channels] fp32 is the state carried in; h_last, a preallocated
     tensor of the same shape (h0 itself will do), receives the state after the last token.
-    workspace: glr_workspace_bytes() bytes, or None for torch's."""
+    workspace: glr_workspace_bytes() bytes (packed: glr_packed_workspace_bytes() will do), or None
+    for torch's."""
     import torch
     dt, (B, T, D) = _in_dtype(x), _glr_shape(x, cu_seqlens, T)
     dev, f32 = x.device, torch.float32
@@ -695,7 +710,7 @@ def glr_forward(x, log_a, *, h0=None, h_last=None, cu_seqlens=None, T: Optional[
     if out is None:
         out = _like(log_a, stream)
     h = _expect(out, "out", f32, x.shape, dev)
-    ws, at, size = _workspace(workspace, _glr_need(B, T, D), log_a, stream)
+    ws, at, size = _workspace(workspace, _glr_need(B, T, D, None if cu is None else log_a.shape[0]), log_a, stream)
     _on_device(lib().llattn_glr_fwd, dev, stream, "llattn_glr_fwd",
                (dt, x.data_ptr(), la, states[0], h, states[1], B, T, D, cu, at, size))
     return out
@@ -723,7 +738,7 @@ def glr_backward(log_a, h, dh, *, h0=None, dh_last=None, cu_seqlens=None, T: Opt
     outs = (_expect(grads["x"], "grads['x']", f32, shape, dev),
             _expect(grads["log_a"], "grads['log_a']", f32, shape, dev),
             _expect_state(grads.get("h0"), "grads['h0']", B * D, dev))
-    ws, at, size = _workspace(workspace, _glr_need(B, T, D), log_a, stream)
+    ws, at, size = _workspace(workspace, _glr_need(B, T, D, None if cu is None else log_a.shape[0]), log_a, stream)
     _on_device(lib().llattn_glr_bwd, dev, stream, "llattn_glr_bwd",
                (*ins, *outs, B, T, D, cu, at, size))
     return grads

@@ -884,12 +884,20 @@ llattn_status llattn_glr_workspace_bytes(int B, int T, int D, size_t* bytes) {
   return LLATTN_OK;
 }
 
+llattn_status llattn_glr_packed_workspace_bytes(int B, int T, long long rows, int D, size_t* bytes) {
+  if (!bytes) return LLATTN_ERR_ARG;
+  if (B < 0 || T < 0 || D < 0 || B > 65535 || D > 65535 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
+  if (rows < 0 || rows > 0x7fffffffll || (unsigned long long)rows > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
+  *bytes = B == 0 || D == 0 ? 0 : llattn::glr_packed_workspace_bytes(B, T, rows, D);
+  return LLATTN_OK;
+}
+
 llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float* log_a, const float* h0,
                              float* h, float* h_last, int B, int T, int D, const int* cu_seqlens,
                              void* workspace, size_t workspace_bytes, void* stream) {
   if (in_dtype != LLATTN_F32 && in_dtype != LLATTN_BF16) return LLATTN_ERR_DTYPE;
   if (B < 0 || T < 0 || D < 0 || B > 65535 || D > 65535 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
-  if ((unsigned long long)B * T > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
+  if (!cu_seqlens && (unsigned long long)B * T > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
   if (B == 0 || D == 0 || (T == 0 && !h_last)) return LLATTN_OK;  // nothing to compute
   if (T > 0 && (!x || !log_a || !h)) return LLATTN_ERR_ARG;
   const size_t e = in_dtype == LLATTN_BF16 ? 2 : 4;
@@ -908,11 +916,12 @@ llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float* log_a, co
   if (s != LLATTN_OK) return s;
   void* ws = nullptr;
   std::unique_lock<std::mutex> lock(g_mu, std::defer_lock);
-  if ((s = pick_workspace(ds, llattn::glr_workspace_bytes(B, T, D), workspace, workspace_bytes, lock,
-                          &ws)) != LLATTN_OK)
-    return s;
+  const size_t all = llattn::glr_workspace_bytes(B, T, D);
+  // (a caller's for a packed batch may be sized by its rows, which only the kernel can check)
+  const size_t need = workspace && cu_seqlens ? llattn::glr_packed_workspace_bytes(B, T, 0, D) : all;
+  if ((s = pick_workspace(ds, need, workspace, workspace_bytes, lock, &ws)) != LLATTN_OK) return s;
   llattn::GlrProblem p{in_dtype, x, log_a, h0, h, h_last, B, T, D, cu_seqlens, ds->status};
-  const cudaError_t err = llattn::glr_forward(p, ws, static_cast<cudaStream_t>(stream));
+  const cudaError_t err = llattn::glr_forward(p, ws, workspace ? workspace_bytes : all, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
 }
 
@@ -921,7 +930,7 @@ llattn_status llattn_glr_bwd(const float* log_a, const float* h, const float* h0
                              int T, int D, const int* cu_seqlens, void* workspace,
                              size_t workspace_bytes, void* stream) {
   if (B < 0 || T < 0 || D < 0 || B > 65535 || D > 65535 || T > (1 << 24)) return LLATTN_ERR_SHAPE;
-  if ((unsigned long long)B * T > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
+  if (!cu_seqlens && (unsigned long long)B * T > kMaxElements / (D ? D : 1)) return LLATTN_ERR_SHAPE;
   if (B == 0 || D == 0 || (T == 0 && !dh0)) return LLATTN_OK;  // nothing to compute
   if (T > 0 && (!log_a || !h || !dh || !dx || !dlog_a)) return LLATTN_ERR_ARG;
   const void* ptrs[9] = {log_a, h, h0, dh, dh_last, dx, dlog_a, dh0, cu_seqlens};
@@ -938,12 +947,13 @@ llattn_status llattn_glr_bwd(const float* log_a, const float* h, const float* h0
   if (s != LLATTN_OK) return s;
   void* ws = nullptr;
   std::unique_lock<std::mutex> lock(g_mu, std::defer_lock);
-  if ((s = pick_workspace(ds, llattn::glr_workspace_bytes(B, T, D), workspace, workspace_bytes, lock,
-                          &ws)) != LLATTN_OK)
-    return s;
+  const size_t all = llattn::glr_workspace_bytes(B, T, D);
+  // (a caller's for a packed batch may be sized by its rows, which only the kernel can check)
+  const size_t need = workspace && cu_seqlens ? llattn::glr_packed_workspace_bytes(B, T, 0, D) : all;
+  if ((s = pick_workspace(ds, need, workspace, workspace_bytes, lock, &ws)) != LLATTN_OK) return s;
   llattn::GlrBwdProblem p{log_a, h, h0, dh, dh_last, dx, dlog_a, dh0, B, T, D, cu_seqlens,
                           ds->status};
-  const cudaError_t err = llattn::glr_backward(p, ws, static_cast<cudaStream_t>(stream));
+  const cudaError_t err = llattn::glr_backward(p, ws, workspace ? workspace_bytes : all, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? LLATTN_OK : cuda_fail(err);
 }
 

@@ -23,14 +23,14 @@
 //
 // What bounds it: memory traffic (10 bytes per element forward with bf16 x, 20 backward), as long
 // as enough CTAs are resident to hide a tile's chain of copy, join, look-back and store.  Three
-// CTAs of 256 threads with one tile each in flight carry 134 M elements in 255 us as one sequence
-// of 65536 steps and in 248 us as eight (5.3 and 5.4 TB/s), and gradients of 95 M elements in eight
-// packed sequences in 332 us (5.7 TB/s).  With the plain product of gates in place of G, and before
+// CTAs of 256 threads with one tile each in flight carry 134 M elements in 248 us as one sequence
+// of 65536 steps and in 235 us as eight (5.4 and 5.7 TB/s), and gradients of 95 M elements in eight
+// packed sequences in 326 us (5.8 TB/s).  With the plain product of gates in place of G, and before
 // tiles went by turns (below), three CTAs took 262 and 239 us forward, two CTAs with the next tile
 // copied ahead 289 and 284, tiles held in registers 300 and 288, and clusters of eight CTAs that
 // walk a sequence side by side and pass the state through distributed shared memory 285 and 298:
 // they leave SMs idle at every shape that is no multiple of their waves.  Maps joined value by value
-// in place of two by two take 264 and 260.  With 32 channels a row of a tile is one 128-byte line of log_a;
+// in place of two by two took 264 and 260 where two by two took 255 and 248.  With 32 channels a row of a tile is one 128-byte line of log_a;
 // 64 and 128 channels made fewer and larger tiles and no better use of memory.
 //
 // Look-back.  A tile publishes its map (32 channels: one 16-byte record each, written and read
@@ -257,42 +257,91 @@ __device__ __forceinline__ Record wait_for(Record x, const Record* r, unsigned w
   }
 }
 
-// The scratch of a call: the counter that hands out tiles, then the records, by (time tile,
-// sequence, channel tile, channel).  Zeroed before the kernel.
+// The scratch of a call: the counter that hands out tiles, then the records, by (slot, channel tile,
+// channel).  Zeroed before the kernel.  A tile's slot is its place among the sequences' tiles, at
+// most ceil(T / TT) each, dense or where a packed batch has room for that many; or, by the rows before
+// its sequence, floor(rows / TT) + the sequences before + its own number: no two alike, and no more
+// than the batch's rows / TT + sequences however long T is.  64 packed sequences, one of 65536 x 2048
+// and 63 of 100, take 305 us forward and 494 backward; with slots and numbers for 64 times 65536 steps
+// they took 3188 and 5228, most of it for zeroing and for numbers of missing tiles.
 struct Scratch {
   unsigned* next;
   Record* rec;
+  long long slots;       // of the records given
+  int tiles, cts;        // ceil(T / TT) at most in a sequence; channel tiles
 };
 constexpr size_t kScratchHead = 256;
 
-// A tile: time tile k of sequence b, 32 channels from ct * 32; the sequence's first row and length.
+// How a call's tiles are numbered: time tile by time tile over all sequences, or (by_seq: where most of
+// those would be missing) slot by slot.  Either way each comes after all that it looks back at.
+struct Plan {
+  unsigned total;        // numbers to hand out; 0: the scratch is too small, nothing is computed
+  int first, stride;     // slots by rows: cu_seqlens[0] and 1, else the sequences' count from one time tile to the next
+  bool by_seq;
+};
+
+// A tile: time tile k of sequence b, 32 channels from ct * 32; the sequence's first row, length and slot.
 // k < 0: no more tiles.
 struct Job {
-  int k, b, ct, len;
+  int k, b, ct, len, slot;
   long long start;
 };
 
-// The CTA's next tile: time tile by time tile, so that it comes after all that it looks back at.  By
-// the counter `next`, or where there is none by turns (the grid's CTAs are then all resident, or no
-// tile looks back).
+// (all threads of a CTA)
+template <int TT, int NT>
+__device__ __forceinline__ Plan make_plan(const Scratch& ws, int nseq, const int* cu, unsigned int* status) {
+  const long long all = (long long)ws.tiles * nseq;
+  if (cu == nullptr || ws.tiles == 1) return {(unsigned)(all * ws.cts), 0, nseq, false};
+  bool up = true;
+  for (int i = threadIdx.x; i < nseq; i += NT) up = up && __ldg(cu + i + 1) >= __ldg(cu + i);
+  up = __syncthreads_and(up);
+  const int first = __ldg(cu);
+  const long long some = ((long long)__ldg(cu + nseq) - first) / TT + nseq;
+  if (up && some <= ws.slots) {
+    const bool by_seq = all > 2 * some || all * ws.cts > 0xffffffffll - (1 << 20);
+    return {(unsigned)((by_seq ? some : all) * ws.cts), first, 1, by_seq};
+  }
+  if (all <= ws.slots && all * ws.cts <= 0xffffffffll - (1 << 20)) return {(unsigned)(all * ws.cts), 0, nseq, false};
+  if (threadIdx.x == 0) atomicOr(status, LLATTN_DEV_WORKSPACE);
+  return {0u, 0, 1, false};
+}
+
+// The CTA's next tile, by the counter `next`, or where there is none by turns (the grid's CTAs are then
+// all resident, or no tile looks back).
 template <int TT>
-__device__ __forceinline__ Job take_job(unsigned* next, unsigned& turn, unsigned total, int nseq,
-                                        int cts, int T, const int* cu, unsigned int* status) {
-  const unsigned per = (unsigned)nseq * cts;
+__device__ __forceinline__ Job take_job(const Scratch& ws, const Plan& pl, unsigned& turn, int nseq, int T,
+                                        const int* cu, unsigned int* status) {
+  auto slot_of = [&](int b) { return (int)((unsigned)(__ldg(cu + b) - pl.first) / (unsigned)TT) + b; };
   for (;;) {
     unsigned i;
-    if (next) {
-      i = atomicAdd(next, 1u);
+    if (ws.next) {
+      i = atomicAdd(ws.next, 1u);
     } else {
       i = turn;
       turn += gridDim.x;
     }
-    if (i >= total) return {-1, 0, 0, 0, 0};
-    const unsigned k = i / per, r = i - k * per;
-    const int b = (int)(r / cts);
+    if (i >= pl.total) return {-1, 0, 0, 0, 0, 0};
+    int k, b, slot;
+    const unsigned at = i / ws.cts;
+    const int ct = (int)(i % ws.cts);
+    if (pl.by_seq) {               // the last sequence whose slots start at or before it
+      int lo = 0, hi = nseq;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((unsigned)slot_of(mid) <= at) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      slot = slot_of(b);
+      k = (int)at - slot;
+    } else {
+      k = (int)(at / nseq);
+      b = (int)(at % nseq);
+      slot = pl.stride == 1 && cu ? slot_of(b) : b;
+    }
     const SeqSpan sp = seq_span(b, T, cu, status);
-    if ((int)k * TT < sp.len || k == 0)   // past a shorter sequence's end there is no tile
-      return {(int)k, b, (int)(r % cts), sp.len, sp.start};
+    if (k == 0 || (long long)k * TT < sp.len)   // past a sequence's end there is no tile
+      return {k, b, ct, sp.len, slot, sp.start};
   }
 }
 
@@ -304,6 +353,7 @@ struct Shared {
   } map[2];      // the warps' maps, then those of the warps before each (a warp may be a tile ahead)
   float in[kCT];
   Job job[4];    // a ring: the present tile, the next, the one being taken
+  Plan plan;
 };
 
 // Joins the threads' maps of a tile (VEC channels of S steps each) over their warps, and the warps'
@@ -348,7 +398,7 @@ __device__ __forceinline__ void join_warps(Shared<NT>& sh, int it, float (&G)[VE
 // returns what leaves the tile.
 template <int NT>
 __device__ __forceinline__ float look_back(Shared<NT>& sh, int it, const Job& at, float start, bool last,
-                                           int nseq, int cts, Record* rec, unsigned int* status) {
+                                           const Scratch& ws, unsigned int* status) {
   const int lane = threadIdx.x & 31;
   float g = 0.f, h = 0.f, in = start;
 #pragma unroll
@@ -361,8 +411,8 @@ __device__ __forceinline__ float look_back(Shared<NT>& sh, int it, const Job& at
   }
   if (at.k > 0 || !last) {
     // records of this sequence and channel, by time tile
-    const size_t step = (size_t)nseq * cts * kCT;
-    Record* r = rec + ((size_t)at.b * cts + at.ct) * kCT + lane;
+    const size_t step = (size_t)sh.plan.stride * ws.cts * kCT;
+    Record* r = ws.rec + ((size_t)at.slot * ws.cts + at.ct) * kCT + lane;
     if (at.k > 0) {
       if (!last) publish(r + at.k * step, g, h, 0.f, kMap);
       // the tile whose outcome is taken (the sequence's first, or the last of the group before),
@@ -406,22 +456,26 @@ __device__ __forceinline__ void enter(const Shared<NT>& sh, int it, const float 
 }
 
 template <typename T, int NT, int VEC, int S>
-struct FwdShared {
+struct FwdShared {           // (rows on lines of 128 bytes: 16 bytes off, asynchronous copies of 65536 x 2048 take 8% longer)
   Shared<NT> sh;
-  Floats<VEC> a[S][NT];      // log_a, then the gates
-  Raw<T, VEC> x[S][NT];
+  alignas(128) Floats<VEC> a[S][NT];   // log_a, then the gates
+  alignas(128) Raw<T, VEC> x[S][NT];
 };
 
 template <typename T, int NT, int VEC, int S, int MINB>
-__global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch ws, int cts, unsigned total) {
+__global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch ws) {
   constexpr int LPR = kCT / VEC, TT = NT / LPR * S;
-  extern __shared__ float4 smem[];
+  extern __shared__ __align__(128) float4 smem[];
   FwdShared<T, NT, VEC, S>& sm = *reinterpret_cast<FwdShared<T, NT, VEC, S>*>(smem);
   Shared<NT>& sh = sm.sh;
   const int tid = threadIdx.x, lane = tid & 31, slot = tid / LPR, cv = tid % LPR * VEC;
   const T* xs = static_cast<const T*>(p.x);
   unsigned turn = blockIdx.x;
-  auto take = [&] { return take_job<TT>(ws.next, turn, total, p.nseq, cts, p.T, p.cu_seqlens, p.status); };
+  {
+    const Plan pl = make_plan<TT, NT>(ws, p.nseq, p.cu_seqlens, p.status);
+    if (tid == 32) sh.plan = pl;   // (what the other threads read of it is read behind a barrier)
+  }
+  auto take = [&] { return take_job<TT>(ws, sh.plan, turn, p.nseq, p.T, p.cu_seqlens, p.status); };
   auto copy = [&](const Job& j) {
     const int t0 = j.k * TT + slot * S, c = j.ct * kCT + cv, n = j.k >= 0 && c < p.D ? j.len - t0 : 0;
     const long long o = (j.start + t0) * p.D + c;
@@ -492,7 +546,7 @@ __global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch 
     __syncthreads();
     if (tid == 32 && sh.job[(it + 1) & 3].k >= 0) sh.job[(it + 2) & 3] = take();
     if (tid < 32) {
-      const float out = look_back<NT>(sh, it, at, start, last, p.nseq, cts, ws.rec, p.status);
+      const float out = look_back<NT>(sh, it, at, start, last, ws, p.status);
       if (last && p.h_last && cl < p.D) p.h_last[state] = out;
     }
     __syncthreads();
@@ -527,21 +581,25 @@ __global__ void __launch_bounds__(NT, MINB) glr_fwd_tiles(GlrProblem p, Scratch 
 template <int NT, int VEC, int S>
 struct BwdShared {
   Shared<NT> sh;
-  Floats<VEC> a[S][NT];      // log_a, then the gates
-  Floats<VEC> dh[S][NT], h[S][NT];
+  alignas(128) Floats<VEC> a[S][NT];   // log_a, then the gates
+  alignas(128) Floats<VEC> dh[S][NT], h[S][NT];
 };
 
 // Backward in time, counted from the sequence's end: c_t = a_t (dh_t + c_{t+1}), c after the last
 // step being dh_last, so that g_t = dh_t + c_{t+1} and dlog_a_t = c_t h_{t-1}.
 template <int NT, int VEC, int S, int MINB>
-__global__ void __launch_bounds__(NT, MINB) glr_bwd_tiles(GlrBwdProblem p, Scratch ws, int cts, unsigned total) {
+__global__ void __launch_bounds__(NT, MINB) glr_bwd_tiles(GlrBwdProblem p, Scratch ws) {
   constexpr int LPR = kCT / VEC, TT = NT / LPR * S;
-  extern __shared__ float4 smem[];
+  extern __shared__ __align__(128) float4 smem[];
   BwdShared<NT, VEC, S>& sm = *reinterpret_cast<BwdShared<NT, VEC, S>*>(smem);
   Shared<NT>& sh = sm.sh;
   const int tid = threadIdx.x, lane = tid & 31, slot = tid / LPR, cv = tid % LPR * VEC;
   unsigned turn = blockIdx.x;
-  auto take = [&] { return take_job<TT>(ws.next, turn, total, p.nseq, cts, p.T, p.cu_seqlens, p.status); };
+  {
+    const Plan pl = make_plan<TT, NT>(ws, p.nseq, p.cu_seqlens, p.status);
+    if (tid == 32) sh.plan = pl;   // (what the other threads read of it is read behind a barrier)
+  }
+  auto take = [&] { return take_job<TT>(ws, sh.plan, turn, p.nseq, p.T, p.cu_seqlens, p.status); };
   auto copy = [&](const Job& j) {
     const int u0 = j.k * TT + slot * S, c = j.ct * kCT + cv, n = j.k >= 0 && c < p.D ? j.len - u0 : 0;
     const long long o = (j.start + j.len - 1 - u0) * p.D + c;
@@ -610,7 +668,7 @@ __global__ void __launch_bounds__(NT, MINB) glr_bwd_tiles(GlrBwdProblem p, Scrat
     __syncthreads();
     if (tid == 32 && sh.job[(it + 1) & 3].k >= 0) sh.job[(it + 2) & 3] = take();
     if (tid < 32) {
-      const float out = look_back<NT>(sh, it, at, start, last, p.nseq, cts, ws.rec, p.status);
+      const float out = look_back<NT>(sh, it, at, start, last, ws, p.status);
       if (last && p.dh0 && cl < p.D) p.dh0[state] = out;
     }
     __syncthreads();
@@ -700,13 +758,14 @@ constexpr int kWalkT = 16;   // a tile's threads have a step each at best below 
 constexpr int kTileSteps = 64;   // the fewest steps a tile has, which sizes the scratch
 // Sequences times channel tiles up to which tiles are handed out by turns.  A chain of tiles moves
 // at the pace of its slowest, and turns keep neighbours in time in step: one sequence of 65536 x
-// 1024 takes 250 us backward by turns and 340 by the counter, 65536 x 2048 479 and 573.  Many
-// chains hide that, and the counter evens out the SMs: 8 x 9600 x 1024 takes 273 us by the counter
-// and 291 by turns, 32 x 2048 x 1024 240 and 263.
+// 1024 takes 228 us backward by turns and 266 by the counter, of 65536 x 2048 forward 247 and 268.  Many
+// chains hide that, and the counter evens out the SMs: gradients of 8 x 9600 x 1024 take 260 us by the
+// counter and 278 by turns, of 32 x 2048 x 1024 229 and 261.
 constexpr int kFewChains = 128;
 
+size_t slot_bytes(int D) { return (size_t)((D + kCT - 1) / kCT) * kCT * sizeof(Record); }
 size_t scratch_bytes(int nseq, int T, int D, int tt) {
-  return kScratchHead + (size_t)((T + tt - 1) / tt) * nseq * ((D + kCT - 1) / kCT) * kCT * sizeof(Record);
+  return kScratchHead + (size_t)((T + tt - 1) / tt) * nseq * slot_bytes(D);
 }
 
 // What a kernel is asked for once on each device: its shared memory (an opt-in there), and how many
@@ -730,18 +789,18 @@ cudaError_t resident_ctas(Kernel kernel, Resident& held, int threads, size_t sme
 }
 
 template <typename Problem>
-cudaError_t launch_tiles(void (*kernel)(Problem, Scratch, int, unsigned), Resident& held,
-                         const Problem& p, int tt, int threads, size_t smem, void* ws,
-                         cudaStream_t st) {
+cudaError_t launch_tiles(void (*kernel)(Problem, Scratch), Resident& held, const Problem& p, int tt,
+                         int threads, size_t smem, void* ws, size_t ws_bytes, cudaStream_t st) {
   const int cts = (p.D + kCT - 1) / kCT, tiles = (p.T + tt - 1) / tt;
-  Scratch s{static_cast<unsigned*>(ws),
-            reinterpret_cast<Record*>(static_cast<char*>(ws) + kScratchHead)};
-  const unsigned total = (unsigned)tiles * p.nseq * cts;
+  const size_t most_bytes = scratch_bytes(p.nseq, p.T, p.D, tt), bytes = ws_bytes < most_bytes ? ws_bytes : most_bytes;
+  Scratch s{static_cast<unsigned*>(ws), reinterpret_cast<Record*>(static_cast<char*>(ws) + kScratchHead),
+            bytes > kScratchHead ? (long long)((bytes - kScratchHead) / slot_bytes(p.D)) : 0, tiles, cts};
+  const unsigned long long total = (unsigned long long)tiles * p.nseq * cts;
   int most = 0;
   cudaError_t e = resident_ctas(kernel, held, threads, smem, &most);
   if (e != cudaSuccess) return e;
-  if (tiles > 1 && (e = cudaMemsetAsync(ws, 0, scratch_bytes(p.nseq, p.T, p.D, tt), st)) != cudaSuccess) return e;
-  const unsigned grid = total < (unsigned)most ? total : (unsigned)most;
+  if (tiles > 1 && (e = cudaMemsetAsync(ws, 0, bytes, st)) != cudaSuccess) return e;
+  const unsigned grid = total < (unsigned)most ? (unsigned)total : (unsigned)most;
   if (tiles == 1 || p.nseq * (long long)cts <= kFewChains) {
     Scratch turns = s;
     turns.next = nullptr;
@@ -755,29 +814,29 @@ cudaError_t launch_tiles(void (*kernel)(Problem, Scratch, int, unsigned), Reside
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = tiles == 1 ? 0 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, turns, cts, total);
+    return cudaLaunchKernelEx(&cfg, kernel, p, turns);
   }
-  kernel<<<grid, threads, smem, st>>>(p, s, cts, total);
+  kernel<<<grid, threads, smem, st>>>(p, s);
   return cudaGetLastError();
 }
 
 template <typename T, int NT, int VEC, int S, int MINB>
-cudaError_t fwd_tiles(const GlrProblem& p, void* ws, cudaStream_t st) {
+cudaError_t fwd_tiles(const GlrProblem& p, void* ws, size_t ws_bytes, cudaStream_t st) {
   static Resident held;
   return launch_tiles(glr_fwd_tiles<T, NT, VEC, S, MINB>, held, p, NT * VEC / kCT * S, NT,
-                      sizeof(FwdShared<T, NT, VEC, S>), ws, st);
+                      sizeof(FwdShared<T, NT, VEC, S>), ws, ws_bytes, st);
 }
 template <int NT, int VEC, int S, int MINB>
-cudaError_t bwd_tiles(const GlrBwdProblem& p, void* ws, cudaStream_t st) {
+cudaError_t bwd_tiles(const GlrBwdProblem& p, void* ws, size_t ws_bytes, cudaStream_t st) {
   static Resident held;
   return launch_tiles(glr_bwd_tiles<NT, VEC, S, MINB>, held, p, NT * VEC / kCT * S, NT,
-                      sizeof(BwdShared<NT, VEC, S>), ws, st);
+                      sizeof(BwdShared<NT, VEC, S>), ws, ws_bytes, st);
 }
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 template <typename T>
-cudaError_t fwd(const GlrProblem& p, void* ws, cudaStream_t st) {
+cudaError_t fwd(const GlrProblem& p, void* ws, size_t ws_bytes, cudaStream_t st) {
   if (p.T <= kWalkT) {
     const dim3 grid((p.D + kWalkThreads - 1) / kWalkThreads, p.nseq);
     glr_fwd_walk<T><<<grid, kWalkThreads, 0, st>>>(p);
@@ -785,11 +844,11 @@ cudaError_t fwd(const GlrProblem& p, void* ws, cudaStream_t st) {
   }
   const bool vec = p.D % 4 == 0 && aligned_to(p.x, 4 * sizeof(T)) && aligned_to(p.log_a, 16) &&
                    aligned_to(p.h, 16);
-  // Eight steps of four channels a thread: seven take 278 us for one sequence of 65536 x 2048, nine 257 (and
-  // 143 for 132 at 32 x 2048 x 1024, whose last tile is then short), twelve with two CTAs to an SM 257
-  // (and 271 for 258 at 8 x 8192 x 2048), six with three CTAs 289.
-  if (!vec) return fwd_tiles<T, 128, 1, 32, 4>(p, ws, st);
-  return fwd_tiles<T, 256, 4, 8, 3>(p, ws, st);
+  // Eight steps of four channels a thread, which took 255 us for one sequence of 65536 x 2048 before rows lay
+  // on lines of 128 bytes (248 now): seven took 278, nine 257 (and 143 for 132 at 32 x 2048 x 1024, whose
+  // last tile is then short), twelve with two CTAs to an SM 257 (and 271 for 258 at 8 x 8192 x 2048), six 289.
+  if (!vec) return fwd_tiles<T, 128, 1, 32, 4>(p, ws, ws_bytes, st);
+  return fwd_tiles<T, 256, 4, 8, 3>(p, ws, ws_bytes, st);
 }
 
 }  // namespace
@@ -798,12 +857,19 @@ size_t glr_workspace_bytes(int nseq, int T, int D) {
   return T <= kTileSteps ? 0 : scratch_bytes(nseq, T, D, kTileSteps);
 }
 
-cudaError_t glr_forward(const GlrProblem& p, void* ws, cudaStream_t st) {
-  count_launch();
-  return p.in_dtype == LLATTN_BF16 ? fwd<__nv_bfloat16>(p, ws, st) : fwd<float>(p, ws, st);
+size_t glr_packed_workspace_bytes(int nseq, int T, long long rows, int D) {
+  if (T <= kTileSteps) return 0;
+  const size_t all = scratch_bytes(nseq, T, D, kTileSteps);
+  const size_t some = kScratchHead + ((size_t)(rows / kTileSteps) + nseq) * slot_bytes(D);
+  return some < all ? some : all;
 }
 
-cudaError_t glr_backward(const GlrBwdProblem& p, void* ws, cudaStream_t st) {
+cudaError_t glr_forward(const GlrProblem& p, void* ws, size_t ws_bytes, cudaStream_t st) {
+  count_launch();
+  return p.in_dtype == LLATTN_BF16 ? fwd<__nv_bfloat16>(p, ws, ws_bytes, st) : fwd<float>(p, ws, ws_bytes, st);
+}
+
+cudaError_t glr_backward(const GlrBwdProblem& p, void* ws, size_t ws_bytes, cudaStream_t st) {
   count_launch();
   if (p.T <= kWalkT) {
     const dim3 grid((p.D + kWalkThreads - 1) / kWalkThreads, p.nseq);
@@ -813,11 +879,11 @@ cudaError_t glr_backward(const GlrBwdProblem& p, void* ws, cudaStream_t st) {
   const void* ptrs[6] = {p.log_a, p.h, p.h0, p.dh, p.dx, p.dlog_a};
   bool vec = p.D % 4 == 0;
   for (const void* q : ptrs) vec = vec && aligned_to(q, 16);
-  // Five steps a thread with three CTAs to an SM: 457 us for one sequence of 65536 x 2048 and 332 for the
-  // packed 95 M elements above; four steps 486 and 351, with four CTAs (whose registers spill) 515 and 371;
-  // six steps 497 and 368.
-  if (!vec) return bwd_tiles<128, 1, 16, 6>(p, ws, st);
-  return bwd_tiles<256, 4, 5, 3>(p, ws, st);
+  // Five steps a thread with three CTAs to an SM, which took 457 us for one sequence of 65536 x 2048 and 332 for
+  // the packed 95 M elements above before rows lay on lines of 128 bytes (435 and 326 now): four steps took
+  // 486 and 351, with four CTAs (whose registers spill) 515 and 371; six steps 497 and 368.
+  if (!vec) return bwd_tiles<128, 1, 16, 6>(p, ws, ws_bytes, st);
+  return bwd_tiles<256, 4, 5, 3>(p, ws, ws_bytes, st);
 }
 
 }  // namespace llattn

@@ -32,10 +32,12 @@ struct GlrBwdProblem {
   unsigned int* status;
 };
 
-// Scratch of either call (0 where a sequence fits one tile).
+// Scratch of either call (0 where a sequence fits one tile); of a packed batch of that many rows; and the
+// least that a packed call is tried with (its kernel knows the rows).
 size_t glr_workspace_bytes(int nseq, int T, int D);
+size_t glr_packed_workspace_bytes(int nseq, int T, long long rows, int D);
 
-cudaError_t glr_forward(const GlrProblem& p, void* ws, cudaStream_t st);
-cudaError_t glr_backward(const GlrBwdProblem& p, void* ws, cudaStream_t st);
+cudaError_t glr_forward(const GlrProblem& p, void* ws, size_t ws_bytes, cudaStream_t st);
+cudaError_t glr_backward(const GlrBwdProblem& p, void* ws, size_t ws_bytes, cudaStream_t st);
 
 }  // namespace llattn

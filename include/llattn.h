@@ -104,6 +104,8 @@ enum {
   LLATTN_DEV_WAIT_TIMEOUT = 2u,  /* an mbarrier / pipeline wait hit its iteration limit */
   LLATTN_DEV_BAD_CU_SEQLENS = 4u, /* cu_seqlens decreasing */
   LLATTN_DEV_DECODE_POS = 8u,    /* decode step or prefill state: a position outside [0, 2^(L-1)) */
+  LLATTN_DEV_WORKSPACE = 32u,    /* packed recurrence: a workspace too small for the batch's rows;
+                                  * nothing is computed */
   LLATTN_DEV_NONFINITE = 16u     /* tensor-core forward: an output value came out inf or NaN.
                                   * With finite inputs this means an intermediate rounded to
                                   * fp16 (P, V, the decay-scaled K, a level state, Q) left
@@ -525,12 +527,17 @@ LLATTN_API llattn_status llattn_qk_norm_rope_bwd(
  *   workspace  caller-owned device scratch of llattn_glr_workspace_bytes() bytes (256-byte
  *              aligned; its contents do not matter), or NULL for the library's per-device buffer
  *              (as llattn_fwd: calls that overlap need workspaces of their own).  A query of 0
- *              bytes needs none.
+ *              bytes needs none.  That size follows B and T; a packed batch may bring one of
+ *              llattn_glr_packed_workspace_bytes() for its rows (cu_seqlens[B] - cu_seqlens[0], or
+ *              more), so that a long T, or one long sequence among many short ones, costs nothing.
+ *              One too small for the rows sets LLATTN_DEV_WORKSPACE, and nothing is computed.
  * Pointers aligned to their type (16-byte alignment and D a multiple of 4 run fastest); no
  * output may overlap an input or another output, h_last == h0 excepted.  The same call gives the
  * same bits.  Asynchronous on `stream`.
  */
 LLATTN_API llattn_status llattn_glr_workspace_bytes(int B, int T, int D, size_t* bytes);
+LLATTN_API llattn_status llattn_glr_packed_workspace_bytes(int B, int T, long long rows, int D,
+                                                           size_t* bytes);
 LLATTN_API llattn_status llattn_glr_fwd(int in_dtype, const void* x, const float* log_a,
                                         const float* h0, float* h, float* h_last, int B, int T,
                                         int D, const int* cu_seqlens, void* workspace,

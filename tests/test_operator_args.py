@@ -218,3 +218,24 @@ def test_workspace_is_checked():
     for bad in (torch.empty(16)[::2], torch.empty(16, device="meta")):   # strided; of another device
         with pytest.raises(ValueError):
             binding._workspace(bad, 16, like, None)
+
+
+def test_glr_packed_workspace():
+    """What the binding allocates without asking; never more than for any batch of the bound."""
+    for B, T, rows, D in ((64, 65536, 71836, 2048), (3, 64, 100, 33), (3, 65, 100, 33), (8, 16384, 92526, 1024),
+                          (5, 1 << 24, 7, 1), (65535, 1 << 24, 1 << 21, 64), (0, 100, 0, 4), (2, 1000, 0, 4)):
+        n = binding.glr_packed_workspace_bytes(B, T, rows, D)
+        assert n == binding._glr_need(B, T, D, rows), (B, T, rows, D)
+        if B * T * D < 1 << 40:
+            assert n <= binding.glr_workspace_bytes(B, T, D)
+    for bad in ((-1, 1, 1, 1), (1, 1 << 25, 1, 1), (1, 1, 1, 65536), (1, 1, -1, 1), (1, 1, 1 << 31, 1)):
+        with pytest.raises(binding.LLAttnError):
+            binding.glr_packed_workspace_bytes(*bad)
+
+
+def test_glr_packed_bounds():
+    """A packed call's B * T * D is no limit, its rows are; a workspace without a slot per sequence is refused."""
+    big = dict(B=64, T=1 << 24, D=2048, cu=6 * M)
+    assert _call("llattn_glr_fwd", GLR_ORDER, GLR, dict(big, ws=7 * M, wsn=256 + 64 * 64 * 512 - 1, x=None)) == ARG
+    assert _call("llattn_glr_fwd", GLR_ORDER, GLR, dict(big, cu=None)) == SHAPE
+    assert _call("llattn_glr_bwd", GLRB_ORDER, GLRB, dict(big, cu=None)) == SHAPE
