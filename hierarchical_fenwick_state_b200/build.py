@@ -22,8 +22,9 @@ SOURCES = ["llattn_api.cu", "llattn_simt.cu", "llattn_tc.cu", "llattn_noalloc.cu
 HEADERS = ["llattn_internal.h", "llattn_common.cuh", "llattn_tc_ptx.cuh", "llattn_decode.h",
            "llattn_bwd.h", "llattn_gdn.h", "llattn_qknorm.h", "llattn_glr.h",
            "llattn_decode_q8.h"]
-# Built without --use_fast_math: exp of gates near 0 and sines of far positions at full fp32
-# precision, infinities and denormal block exponents as IEEE has them.
+# Built without --use_fast_math: sines of far positions and the 8-bit state's exp at full fp32
+# precision, infinities, NaN and denormal values as IEEE has them.  (The recurrence asks for the fast
+# exponential by name: its file says what that costs.)
 PRECISE = {"llattn_qknorm.cu", "llattn_glr.cu", "llattn_decode_q8.cu"}
 LIB = os.path.join(HERE, "libllattn.so")
 BUILD_DIR = os.path.join(ROOT, "_build")

@@ -31,7 +31,8 @@
 // walk a sequence side by side and pass the state through distributed shared memory 285 and 298:
 // they leave SMs idle at every shape that is no multiple of their waves.  Maps joined value by value
 // in place of two by two took 264 and 260 where two by two took 255 and 248.  With 32 channels a row of a tile is one 128-byte line of log_a;
-// 64 and 128 channels made fewer and larger tiles and no better use of memory.
+// 64 and 128 channels made fewer and larger tiles and no better use of memory.  At 80 registers a
+// thread the wide forms spill 16 to 52 bytes.
 //
 // Look-back.  A tile publishes its map (32 channels: one 16-byte record each, written and read
 // whole, so no fence is needed) before it knows what enters it.  Tiles are grouped by eight in
@@ -753,7 +754,12 @@ __global__ void __launch_bounds__(kWalkThreads) glr_bwd_walk(GlrBwdProblem p) {
   if (p.dh0) p.dh0[at] = back;
 }
 
-constexpr int kWalkT = 16;   // a tile's threads have a step each at best below it
+// Steps up to which a thread walks a channel token by token: most of a tile's threads have none then.  One
+// sequence of 2048 channels takes 6.2 us by tiles at 17 and at 64 steps and 6.3 and 14.4 by walks
+// (gradients 6.2 and 6.2, 4.2 and 10.4).  Many sequences hide a walk's latency: 64 take 43.1 us by tiles
+// and 6.2 by walks at 17 steps, 43.2 and 10.4 at 32, 43.2 and 33.3 at 64, 46.5 and 47.0 at 128, so the rule
+// is good for few sequences and a loss for many of 17 to 64 steps.
+constexpr int kWalkT = 16;
 
 constexpr int kTileSteps = 64;   // the fewest steps a tile has, which sizes the scratch
 // Sequences times channel tiles up to which tiles are handed out by turns.  A chain of tiles moves
