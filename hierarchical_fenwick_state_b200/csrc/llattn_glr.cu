@@ -30,9 +30,9 @@
 // copied ahead 289 and 284, tiles held in registers 300 and 288, and clusters of eight CTAs that
 // walk a sequence side by side and pass the state through distributed shared memory 285 and 298:
 // they leave SMs idle at every shape that is no multiple of their waves.  Maps joined value by value
-// in place of two by two took 264 and 260 where two by two took 255 and 248.  With 32 channels a row of a tile is one 128-byte line of log_a;
-// 64 and 128 channels made fewer and larger tiles and no better use of memory.  At 80 registers a
-// thread the wide forms spill 16 to 52 bytes.
+// took 264 and 260 us where two by two they took 255 and 248.  With 32 channels a row of a tile is one
+// 128-byte line of log_a; 64 and 128 channels made fewer and larger tiles and no better use of
+// memory.  At 80 registers a thread the wide forms spill 16 to 52 bytes.
 //
 // Look-back.  A tile publishes its map (32 channels: one 16-byte record each, written and read
 // whole, so no fence is needed) before it knows what enters it.  Tiles are grouped by eight in
